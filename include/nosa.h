@@ -39,6 +39,17 @@
  *  - A group is gi = b * Hkv + g; query head h of batch b belongs to group
  *    b * Hkv + h / G with G = Hq / Hkv.
  *
+ * 4-bit cache (kv_bits = 4): the pools hold quantised pages. A row (the d values of one token and
+ * KV head) is cut in groups of 32 values x, each with a bf16 scale s = bf16(max|x| / 7) and 4-bit
+ * codes c = 8 + sign(x) floor(|x| / s + 1/2): a value reads back as (c - 8) s. A group with
+ * s < 2^-126 is stored as zeros; one that holds an infinity or a NaN reads back NaN. A page is
+ * [bs][d/2] bytes of codes, then [bs][d/32] bf16 scales: bs * d * 9/16 bytes. In a K row the
+ * 32-bit word at byte c*(d/8) + 4g has the codes of values 32g + 8c + 0..7, in a V row the 16-bit
+ * word at byte r*(d/16) + 2g those of values 32g + 4r + 0..3, lowest bits first. nosa_write_kv
+ * quantises a run of tokens into the pages, nosa_append / nosa_step / nosa_attend the new token,
+ * nosa_read_kv brings tokens back, and the attention reads the pages as they are. Sub-block
+ * means (kc) are over the values that the cache holds.
+ *
  * Notation: bs = block_size, s = sub_block, N = ceil(L / bs) blocks and
  * M = ceil(L / s) sub-blocks for a context of L tokens, k = k_q + k_e,
  * W = ceil(max_blocks / 32), max_sub = max_blocks * bs / s.
@@ -103,6 +114,9 @@ typedef struct nosa_config {
                              microseconds from the waiting kernel's start, in [0, 60000000];
                              0 = 4 s. A wait that runs out sets NOSA_ERR_TIMEOUT and the kernel
                              returns; nosa_check_device then reports NOSA_ETIMEOUT. */
+  int32_t kv_bits;        /* bits per value of the K and V pools, host pools included: 0 (or 16) =
+                             bf16 pages, 4 = quantised pages (above). Early stop (stop_tau > 0)
+                             needs bf16 pages. */
 } nosa_config;
 
 #define NOSA_SCORE_WINDOW 1
@@ -114,7 +128,9 @@ typedef struct nosa_config {
  * row-major. Without host pools page gi * max_blocks + j holds block j of group
  * gi (the caller writes the prefill there before nosa_state_init). With host
  * pools the host copy is the full backing store, [B*Hkv][max_blocks][bs][d],
- * and the block table maps resident blocks to HBM pages gi * slots + z.
+ * and the block table maps resident blocks to HBM pages gi * slots + z. With kv_bits = 4 a page
+ * is bs * d * 9/16 bytes in the layout above, at the same page numbers; nosa_write_kv writes the
+ * prefill.
  */
 typedef struct nosa_state {
   int32_t* seq_len;       /* [B*Hkv] tokens in the cache */
@@ -157,6 +173,34 @@ nosa_status nosa_workspace_init(void* workspace, size_t ws_bytes, void* stream);
  */
 nosa_status nosa_state_init(const nosa_config* cfg, const nosa_state* st, const int32_t* prefill_len,
                             const uint8_t* resident, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A run of tokens into the 4-bit cache, and back (kv_bits = 4; NOSA_EINVAL otherwise: bf16 pages
+ * are written directly). k, v: device bf16, row of token t and KV head h at
+ * k + t * k_tok + h * k_head (strides in values, multiples of 8; NULL strides = [n_tokens][Hkv][d]
+ * contiguous); the d values of a row are contiguous and 16-byte aligned. The run holds the
+ * sequences' tokens one after the other: token t belongs to sequence b with
+ * cu_tokens[b] <= t < cu_tokens[b + 1] (device int32 [B + 1], ascending) and sits at position
+ * start[b] + t - cu_tokens[b] of it (start: device int32 [B], NULL = 0), so a prompt may come in
+ * one call or in chunks. Tokens of no sequence are skipped (nosa_read_kv leaves their rows as they
+ * were); a position outside [0, max_blocks * block_size) is skipped and sets NOSA_ERR_FULL.
+ *
+ * nosa_write_kv quantises the rows into the pages: the device pools, or with host pools the host
+ * copy (over UVA). It changes nothing else: write the prefill, then call nosa_state_init, which
+ * clears the error word (call nosa_check_device before it to see a write's fault). Reading is the
+ * same call with k and v as outputs, from the same pools; rows must not overlap. n_tokens * Hkv
+ * < 2^30.
+ */
+typedef struct nosa_kv_strides {
+  int64_t k_tok, k_head, v_tok, v_head;
+} nosa_kv_strides;
+
+nosa_status nosa_write_kv(const nosa_config* cfg, const nosa_state* st, const uint16_t* k,
+                          const uint16_t* v, const nosa_kv_strides* strides, int32_t n_tokens,
+                          const int32_t* cu_tokens, const int32_t* start, void* stream);
+nosa_status nosa_read_kv(const nosa_config* cfg, const nosa_state* st, uint16_t* k, uint16_t* v,
+                         const nosa_kv_strides* strides, int32_t n_tokens, const int32_t* cu_tokens,
+                         const int32_t* start, void* stream);
 
 /*
  * Append one token per group: k_new, v_new device bf16 [B*Hkv][d] become token

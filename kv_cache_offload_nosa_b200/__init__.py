@@ -32,7 +32,7 @@ EXPORTS = ("nosa_state_sizes", "nosa_workspace_size", "nosa_workspace_init", "no
            "nosa_append", "nosa_score_blocks", "nosa_select", "nosa_gather", "nosa_decode_attn",
            "nosa_step", "nosa_check_device", "nosa_status_string", "nosa_last_error",
            "nosa_decode_attn_noalloc", "nosa_uva_read_probe", "nosa_plan_ahead", "nosa_prefetch", "nosa_attend", "nosa_stop_counts",
-           "nosa_step_launches", "nosa_step_geometry")
+           "nosa_step_launches", "nosa_step_geometry", "nosa_write_kv", "nosa_read_kv")
 
 
 NOSA_SCORE_WINDOW, NOSA_SCORE_SOFTMAX = 1, 2
@@ -45,7 +45,8 @@ class nosa_config(ctypes.Structure):
                                                              ("score_mode", ctypes.c_int32),
                                                              ("stop_tau", ctypes.c_float),
                                                              ("kc_bf16", ctypes.c_int32),
-                                                             ("wait_us", ctypes.c_int32)]
+                                                             ("wait_us", ctypes.c_int32),
+                                                             ("kv_bits", ctypes.c_int32)]
 
 
 STATE_FIELDS = ("seq_len", "kc", "prev_sel", "alive", "last_used", "block_table", "slot_owner",
@@ -99,6 +100,8 @@ def load(path: Optional[str] = None):
         "nosa_stop_counts": [cfgp, vp, sz, vp, vp],
         "nosa_attend": [cfgp, stp, vp, vp, vp, vp, vp, vp, sz, vp],
         "nosa_step_launches": [cfgp, stp, ctypes.POINTER(ctypes.c_int32)],
+        "nosa_write_kv": [cfgp, stp, vp, vp, vp, ctypes.c_int32, vp, vp, vp],
+        "nosa_read_kv": [cfgp, stp, vp, vp, vp, ctypes.c_int32, vp, vp, vp],
         "nosa_step_geometry": [cfgp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp],
     }
     for name, args in sig.items():
@@ -139,12 +142,12 @@ def _stream(stream) -> Optional[int]:
 
 def make_config(B, Hq, Hkv, d, block_size, sub_block, k_q, k_e, max_blocks, slots=None,
                 n_score_rows=None, attn_split=0, scale=None, score_mode=0, stop_tau=0.0,
-                kc_bf16=0, wait_us=0) -> nosa_config:
+                kc_bf16=0, wait_us=0, kv_bits=0) -> nosa_config:
     G = Hq // Hkv
     return nosa_config(B, Hq, Hkv, d, block_size, sub_block, k_q, k_e, max_blocks,
                        max_blocks if slots is None else slots, G if n_score_rows is None else n_score_rows,
                        attn_split, (1.0 / d ** 0.5) if scale is None else scale, score_mode, stop_tau,
-                       kc_bf16, wait_us)
+                       kc_bf16, wait_us, kv_bits)
 
 
 def state_sizes(cfg: nosa_config) -> nosa_sizes:
@@ -166,6 +169,30 @@ def workspace_init(ws, nbytes: int, stream=None):
 def state_init(cfg, st: nosa_state, prefill_len, resident, ws, ws_bytes, stream=None):
     _check(load().nosa_state_init(ctypes.byref(cfg), ctypes.byref(st), _ptr(prefill_len),
                                   _ptr(resident), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+class nosa_kv_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("k_tok", "k_head", "v_tok", "v_head")]
+
+
+def write_kv(cfg, st, k, v, cu_tokens, start=None, n_tokens=None, strides=None, stream=None):
+    """Quantises a run of tokens' K and V rows into the pages of a 4-bit cache.
+
+    k, v: device bf16 rows, strides (in values) as nosa_kv_strides or None for contiguous
+    [n_tokens][Hkv][d]; n_tokens defaults to k.shape[0].
+    """
+    n = k.shape[0] if n_tokens is None else n_tokens
+    _check(load().nosa_write_kv(ctypes.byref(cfg), ctypes.byref(st), _ptr(k), _ptr(v),
+                                ctypes.byref(strides) if strides is not None else None, n,
+                                _ptr(cu_tokens), _ptr(start), _stream(stream)))
+
+
+def read_kv(cfg, st, k, v, cu_tokens, start=None, n_tokens=None, strides=None, stream=None):
+    """Reads a run of tokens of a 4-bit cache back into the bf16 rows k and v."""
+    n = k.shape[0] if n_tokens is None else n_tokens
+    _check(load().nosa_read_kv(ctypes.byref(cfg), ctypes.byref(st), _ptr(k), _ptr(v),
+                               ctypes.byref(strides) if strides is not None else None, n,
+                               _ptr(cu_tokens), _ptr(start), _stream(stream)))
 
 
 def append(cfg, st, k_new, v_new, stream=None):

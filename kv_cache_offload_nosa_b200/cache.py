@@ -9,9 +9,9 @@ from typing import Optional
 
 import torch
 
-from . import (nosa_config, nosa_state, STATE_FIELDS, state_sizes, workspace_size, workspace_init,
+from . import (nosa_config, nosa_kv_strides, nosa_state, STATE_FIELDS, state_sizes, workspace_size, workspace_init,
                state_init, append, score_blocks, select, gather, decode_attn, step, check_device,
-               plan_ahead, prefetch, attend, stop_counts, NosaError, NOSA_EINVAL)
+               plan_ahead, prefetch, attend, stop_counts, write_kv, read_kv, NosaError, NOSA_EINVAL)
 
 _DTYPE = {"seq_len": torch.int32, "kc": torch.float32, "prev_sel": torch.int32,
           "alive": torch.int32, "last_used": torch.int32, "block_table": torch.int32,
@@ -28,7 +28,33 @@ def buffer_bytes(cfg: nosa_config) -> dict:
             "score_rows": ng * cfg.n_score_rows * cfg.d * 2,
             "block_scores": ng * cfg.max_blocks * 4, "evict": ng * cfg.max_blocks * 4,
             "sel": ng * k * 4, "miss_count": ng * 4, "used": cfg.B * cfg.Hq * 4,
-            "prefill_len": cfg.B * 4, "resident": ng * cfg.max_blocks}
+            "prefill_len": cfg.B * 4, "resident": ng * cfg.max_blocks,
+            "cu_tokens": (cfg.B + 1) * 4, "start": cfg.B * 4}
+
+
+def run_strides(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor,
+                device: torch.device) -> nosa_kv_strides:
+    """Strides of a run's K and V rows; refuses (NosaError, NOSA_EINVAL) tensors that are not
+    [n_tokens, Hkv, d] of 16-bit values on `device` with contiguous rows."""
+    for name, t in (("k", k), ("v", v)):
+        if not t.is_cuda or t.device != device:
+            raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
+        if t.dtype not in (torch.bfloat16, torch.int16):
+            raise NosaError(NOSA_EINVAL, f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
+        if t.dim() != 3 or tuple(t.shape[1:]) != (cfg.Hkv, cfg.d) or t.shape[0] != k.shape[0]:
+            raise NosaError(NOSA_EINVAL, f"{name} must be [n_tokens, {cfg.Hkv}, {cfg.d}], not {tuple(t.shape)}")
+        if t.stride(2) != 1:
+            raise NosaError(NOSA_EINVAL, f"{name}'s rows must be contiguous")
+    # the stride of a dimension of size 1 says nothing
+    at = [s for t in (k, v) for s in (t.stride(0) if t.shape[0] > 1 else cfg.Hkv * cfg.d,
+                                      t.stride(1) if cfg.Hkv > 1 else cfg.d)]
+    return nosa_kv_strides(*at)
+
+
+def check_int32(**bufs):
+    for name, t in bufs.items():
+        if isinstance(t, torch.Tensor) and t.dtype != torch.int32:
+            raise NosaError(NOSA_EINVAL, f"{name} must be int32, not {t.dtype}")
 
 
 def check_buffer(name: str, t, nbytes: int, device: Optional[torch.device] = None):
@@ -75,6 +101,7 @@ class NosaCache:
                 self.t[name] = torch.empty(n, dtype=dt, device=self.device)
         # the state's own device, with its index (the buffers of every call must be there)
         self.device = self.t["seq_len"].device
+        self.t["err"].zero_()  # a write may come before init, which clears it too
         self.ws_bytes = workspace_size(cfg)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         workspace_init(self.ws, self.ws_bytes)
@@ -88,14 +115,34 @@ class NosaCache:
 
     # views in the documented layouts
     def pool_view(self, name: str) -> torch.Tensor:
+        """A pool as [B*Hkv, pages, block_size, d] 16-bit patterns; of a 4-bit cache as
+        [B*Hkv, pages, page bytes] uint8."""
         c = self.cfg
         G = c.B * c.Hkv
         pages = c.max_blocks if name.startswith("host") else c.slots
+        if c.kv_bits == 4:
+            return self.t[name].view(torch.uint8).view(G, pages, c.block_size * c.d * 9 // 16)
         return self.t[name].view(G, pages, c.block_size, c.d)
 
     def init(self, prefill_len: torch.Tensor, resident: Optional[torch.Tensor] = None, stream=None):
         self._check(prefill_len=prefill_len, resident=resident)
         state_init(self.cfg, self.state, prefill_len, resident, self.ws, self.ws_bytes, stream)
+
+    def write(self, k, v, cu_tokens, start=None, stream=None):
+        """Quantises a run of tokens (k, v [n_tokens, Hkv, d] bf16, any strides with contiguous
+        rows) into the pages of a 4-bit cache; tokens cu_tokens[b] .. cu_tokens[b+1]-1 go to
+        positions start[b], ... of sequence b (start None: 0). Write the prefill, then init."""
+        self._check(cu_tokens=cu_tokens, start=start)
+        check_int32(cu_tokens=cu_tokens, start=start)
+        write_kv(self.cfg, self.state, k, v, cu_tokens, start,
+                 strides=run_strides(self.cfg, k, v, self.device), stream=stream)
+
+    def read(self, k, v, cu_tokens, start=None, stream=None):
+        """Reads a run of tokens of a 4-bit cache back into k, v (as write takes them)."""
+        self._check(cu_tokens=cu_tokens, start=start)
+        check_int32(cu_tokens=cu_tokens, start=start)
+        read_kv(self.cfg, self.state, k, v, cu_tokens, start,
+                strides=run_strides(self.cfg, k, v, self.device), stream=stream)
 
     def append(self, k_new, v_new, stream=None):
         self._check(k_new=k_new, v_new=v_new)

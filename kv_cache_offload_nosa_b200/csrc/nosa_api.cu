@@ -6,8 +6,10 @@
 
 #include "nosa.h"
 #include "nosa_attn.cuh"
+#include "nosa_attn_kv4.cuh"
 #include "nosa_attn_stop.cuh"
 #include "nosa_common.cuh"
+#include "nosa_kv4.cuh"
 #include "nosa_kernels.cuh"
 #include "nosa_select.cuh"
 
@@ -42,6 +44,12 @@ int n_groups(const nosa_config& c) { return c.B * c.Hkv; }
 int max_sub(const nosa_config& c) { return c.max_blocks * (c.block_size / c.sub_block); }
 int words(const nosa_config& c) { return (c.max_blocks + 31) / 32; }
 int kk(const nosa_config& c) { return c.k_q + c.k_e; }
+bool kv4(const nosa_config& c) { return c.kv_bits == 4; }
+size_t page_bytes(const nosa_config& c) {
+  return kv4(c) ? (size_t)kv4_page_bytes(c.block_size, c.d) : (size_t)c.block_size * c.d * 2;
+}
+// Partial slots per group of the split-K attention.
+int part_slots(const nosa_config& c) { return kv4(c) ? kPartialSlots : kPartialSlots; }
 
 nosa_status check_cfg(const nosa_config* cp) {
   NOSA_CHECK(cp, "cfg is NULL");
@@ -74,6 +82,8 @@ nosa_status check_cfg(const nosa_config* cp) {
   NOSA_CHECK(!(c.stop_tau > 0.f) || kk(c) <= kStopMaxK, "early stop supports k <= %d", kStopMaxK);
   NOSA_CHECK(c.scale > 0.f, "scale must be > 0");
   NOSA_CHECK(c.wait_us >= 0 && c.wait_us <= 60000000, "wait_us = %d not in [0, 60000000]", c.wait_us);
+  NOSA_CHECK(c.kv_bits == 0 || c.kv_bits == 16 || c.kv_bits == 4, "kv_bits = %d not 0, 16 or 4", c.kv_bits);
+  NOSA_CHECK(!(kv4(c) && c.stop_tau > 0.f), "early stop needs bf16 pages (kv_bits = 4 and stop_tau > 0)");
   const long long groups = (long long)c.B * c.Hkv;
   NOSA_CHECK(groups * c.slots * c.block_size < (1ll << 31), "too many pool rows for TMA coordinates");
   NOSA_CHECK(groups * kk(c) < (1ll << 31), "too many tasks");
@@ -134,7 +144,7 @@ WsLayout ws_layout(const nosa_config& c) {
   w.cnt_attn = off; off += up256(NG * 4);
   w.copy_list = off; off += up256(NG * (size_t)w.copy_stride * 8);
   w.copy_count = off; off += up256(NG * 4);
-  w.partials = off; off += up256(NG * kPartialSlots * (size_t)G * (c.d + 2) * 4);
+  w.partials = off; off += up256(NG * part_slots(c) * (size_t)G * (c.d + 2) * 4);
   w.ge_mask = off; off += up256(NG * (size_t)words(c) * 4);
   w.sel_flag = off; off += up256(NG * kFlagStride * 4);
   w.copy_cnt = off; off += up256(NG * 4);
@@ -238,14 +248,14 @@ nosa_status score_chunk(const nosa_config& c, int* chunk) {
   return NOSA_OK;
 }
 
-template <int D, bool FUSED, int VARIANT, bool KC16>
+template <int D, bool FUSED, int VARIANT, bool KC16, bool KV4>
 nosa_status launch_score_t(const nosa_config& c, const StepArgs& a0, cudaStream_t s) {
   StepArgs a = a0;
   nosa_status r = score_chunk(c, &a.chunk);
   if (r != NOSA_OK) return r;
   dim3 grid((max_sub(c) + a.chunk - 1) / a.chunk, n_groups(c));
   const size_t dsm = (FUSED ? score_su_offset(c.max_blocks) : 0) + (size_t)a.chunk * 4;
-  auto k = score_kernel<D, FUSED, VARIANT, KC16>;
+  auto k = score_kernel<D, FUSED, VARIANT, KC16, KV4>;
   if (dsm > 48 * 1024) NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsm));
   if (kStepCarveout >= 0)
     NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, kStepCarveout));
@@ -256,8 +266,12 @@ nosa_status launch_score_t(const nosa_config& c, const StepArgs& a0, cudaStream_
 
 template <int D, bool FUSED, int VARIANT>
 nosa_status launch_score_kc(const nosa_config& c, const StepArgs& a, cudaStream_t s) {
-  return c.kc_bf16 ? launch_score_t<D, FUSED, VARIANT, true>(c, a, s)
-                   : launch_score_t<D, FUSED, VARIANT, false>(c, a, s);
+  // the pages' format matters to the fused kernel's append alone
+  if (FUSED && kv4(c))
+    return c.kc_bf16 ? launch_score_t<D, FUSED, VARIANT, true, FUSED>(c, a, s)
+                     : launch_score_t<D, FUSED, VARIANT, false, FUSED>(c, a, s);
+  return c.kc_bf16 ? launch_score_t<D, FUSED, VARIANT, true, false>(c, a, s)
+                   : launch_score_t<D, FUSED, VARIANT, false, false>(c, a, s);
 }
 
 template <bool FUSED>
@@ -267,6 +281,14 @@ nosa_status launch_score(const nosa_config& c, const StepArgs& a, cudaStream_t s
   if (FUSED && c.score_mode)
     return c.d == 128 ? launch_score_kc<128, true, 1>(c, a, s) : launch_score_kc<64, true, 1>(c, a, s);
   return c.d == 128 ? launch_score_kc<128, FUSED, 0>(c, a, s) : launch_score_kc<64, FUSED, 0>(c, a, s);
+}
+
+nosa_status launch_append(const nosa_config& c, const StepArgs& a, cudaStream_t s) {
+  auto k = c.d == 128 ? (kv4(c) ? append_kernel<128, true> : append_kernel<128>)
+                      : (kv4(c) ? append_kernel<64, true> : append_kernel<64>);
+  k<<<n_groups(c), 128, 0, s>>>(a);
+  NOSA_CUDA(cudaGetLastError());
+  return NOSA_OK;
 }
 
 nosa_status launch_sel_kernel(void (*k)(StepArgs), const nosa_config& c, const StepArgs& a,
@@ -295,7 +317,7 @@ nosa_status launch_copy(const nosa_config& c, const nosa_state* st, void* ws, cu
   ca.k_pool = reinterpret_cast<uint4*>(st->k_pool);
   ca.v_pool = reinterpret_cast<uint4*>(st->v_pool);
   ca.max_blocks = c.max_blocks;
-  ca.page_vec = c.block_size * c.d * 2 / 16;
+  ca.page_vec = (int)(page_bytes(c) / 16);
   ca.sel_flag = flags ? ws_at<uint32_t>(ws, w.sel_flag) : nullptr;
   ca.copy_cnt = ws_at<uint32_t>(ws, w.copy_cnt);
   ca.copy_flag = ws_at<uint32_t>(ws, w.copy_flag);
@@ -357,8 +379,10 @@ nosa_status make_pool_map(CUtensorMap* m, const nosa_config& c, void* pool) {
 // Tasks ((group, block) pairs) per attention CTA. split > 0: the caller's width; finest: the
 // smallest width the partial slots allow; otherwise the automatic rule below. target = the
 // resident attention CTAs (SMs x CTAs per SM), stage = bytes of one block's K and V pages.
-int attn_split_for(int split, int k, int total, long long target, int sms, int stage, bool finest) {
-  const int wmin = (k + kPartialSlots - 2) / (kPartialSlots - 1);
+// slots = the partial slots per group.
+int attn_split_for(int split, int k, int total, long long target, int sms, int stage, bool finest,
+                   int slots = kPartialSlots) {
+  const int wmin = (k + slots - 2) / (slots - 1);
   int W = split;
   if (W <= 0 && finest) W = wmin;
   if (W <= 0) {
@@ -498,6 +522,32 @@ nosa_status dispatch_attn(const nosa_config& c, const AttnArgs& a, const CUtenso
   return launch_attn_t<64, 128>(c, a, tk, tv, s, finest, pdl);
 }
 
+// The same attention over 4-bit pages.
+nosa_status launch_attn_kv4(const nosa_config& c, const nosa_state* st, const AttnArgs& a, int pslots,
+                            cudaStream_t s, bool finest, bool pdl) {
+  AttnKv4Args x;
+  x.a = a;
+  x.k_pages = reinterpret_cast<const uint8_t*>(st->k_pool);
+  x.v_pages = reinterpret_cast<const uint8_t*>(st->v_pool);
+  x.bs = c.block_size;
+  x.pslots = pslots;
+  int dev = 0, sms = 0;
+  NOSA_CUDA(cudaGetDevice(&dev));
+  NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  x.a.W = attn_split_for(c.attn_split, a.k, a.total, 4LL * sms, sms, 2 * (int)page_bytes(c), finest, pslots);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((a.total + x.a.W - 1) / x.a.W);
+  lc.blockDim = dim3(128);
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = pdl ? 1 : 0;
+  NOSA_CUDA(cudaLaunchKernelEx(&lc, c.d == 128 ? attn_kv4_kernel<128> : attn_kv4_kernel<64>, x));
+  return NOSA_OK;
+}
+
 // ready: per-group flags the attention waits on (and clears), or NULL to wait for the
 // previous grid as a whole. pdl: may start while the previous kernel on the stream runs.
 // early: the score kernel of the same step publishes each group's query-agnostic blocks
@@ -505,9 +555,6 @@ nosa_status dispatch_attn(const nosa_config& c, const AttnArgs& a, const CUtenso
 nosa_status launch_attn(const nosa_config& c, const nosa_state* st, const uint16_t* q, const int32_t* sel,
                         float* out, void* ws, cudaStream_t s, uint32_t* ready = nullptr,
                         bool pdl = true, bool early = false) {
-  CUtensorMap tk, tv;
-  nosa_status r = make_pool_maps(c, st, &tk, &tv);
-  if (r != NOSA_OK) return r;
   const WsLayout w = ws_layout(c);
   AttnArgs a = attn_args(c, st, q, sel, out, ws_at<float>(ws, w.partials), ws_at<uint32_t>(ws, w.cnt_attn));
   a.sel_flag = ready;
@@ -515,6 +562,11 @@ nosa_status launch_attn(const nosa_config& c, const nosa_state* st, const uint16
     a.att_list = ws_at<int32_t>(ws, w.att_list);
     a.e_flag = ws_at<uint32_t>(ws, w.e_flag);
   }
+  const bool finest = ready != nullptr && has_host(st);
+  if (kv4(c)) return launch_attn_kv4(c, st, a, part_slots(c), s, finest, pdl);
+  CUtensorMap tk, tv;
+  nosa_status r = make_pool_maps(c, st, &tk, &tv);
+  if (r != NOSA_OK) return r;
   if (c.stop_tau > 0.f) {
     // early stop: one CTA per group, each waiting for its own group's flag (or the whole grid)
     StopArgs x;
@@ -530,7 +582,6 @@ nosa_status launch_attn(const nosa_config& c, const nosa_state* st, const uint16
     if (c.block_size == 64) return launch_attn_stop_t<64, 64>(c, a, x, tk, tv, s, pdl);
     return launch_attn_stop_t<64, 128>(c, a, x, tk, tv, s, pdl);
   }
-  const bool finest = ready != nullptr && has_host(st);
   return dispatch_attn(c, a, tk, tv, s, finest, pdl);
 }
 
@@ -566,9 +617,9 @@ nosa_status nosa_state_sizes(const nosa_config* cfg, nosa_sizes* out) {
   out->last_used = NG * c.max_blocks * 4;
   out->block_table = NG * c.max_blocks * 4;
   out->slot_owner = NG * c.slots * 4;
-  out->k_pool = NG * c.slots * (size_t)c.block_size * c.d * 2;
+  out->k_pool = NG * c.slots * page_bytes(c);
   out->v_pool = out->k_pool;
-  out->host_k = NG * c.max_blocks * (size_t)c.block_size * c.d * 2;
+  out->host_k = NG * c.max_blocks * page_bytes(c);
   out->host_v = out->host_k;
   out->err = 4;
   return NOSA_OK;
@@ -623,7 +674,11 @@ nosa_status nosa_state_init(const nosa_config* cfg, const nosa_state* st, const 
   const int ppg = has_host(st) ? c.max_blocks : c.slots;
   const int subs = 256 / c.d * 4;
   dim3 g((max_sub(c) + subs - 1) / subs, n_groups(c));
-  if (c.d == 128)
+  if (kv4(c)) {
+    auto k = c.d == 128 ? (c.kc_bf16 ? init_kc_kernel<128, true, true> : init_kc_kernel<128, false, true>)
+                        : (c.kc_bf16 ? init_kc_kernel<64, true, true> : init_kc_kernel<64, false, true>);
+    k<<<g, 256, 0, s>>>(prefill_len, c.Hkv, src, ppg, st->kc, max_sub(c), c.block_size, c.sub_block);
+  } else if (c.d == 128)
     if (c.kc_bf16) init_kc_kernel<128, true><<<g, 256, 0, s>>>(prefill_len, c.Hkv, src, ppg, st->kc, max_sub(c), c.block_size, c.sub_block);
     else init_kc_kernel<128, false><<<g, 256, 0, s>>>(prefill_len, c.Hkv, src, ppg, st->kc, max_sub(c), c.block_size, c.sub_block);
   else
@@ -632,6 +687,91 @@ nosa_status nosa_state_init(const nosa_config* cfg, const nosa_state* st, const 
   NOSA_CUDA(cudaGetLastError());
   if (has_host(st)) return launch_copy(c, st, ws, s);
   return NOSA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Arguments and checks of nosa_write_kv and nosa_read_kv (out: k and v are written).
+nosa_status kv_run_args(const nosa_config* cfg, const nosa_state* st, const uint16_t* k, const uint16_t* v,
+                        const nosa_kv_strides* strides, int32_t n_tokens, const int32_t* cu_tokens,
+                        const int32_t* start, bool out, KvRunArgs* a) {
+  nosa_status r = check_cfg(cfg);
+  if (r != NOSA_OK) return r;
+  const nosa_config& c = *cfg;
+  if ((r = check_state(c, st)) != NOSA_OK) return r;
+  NOSA_CHECK(kv4(c), "kv_bits = %d: runs of tokens are written to and read from 4-bit caches", c.kv_bits);
+  NOSA_CHECK(n_tokens >= 0 && (long long)n_tokens * c.Hkv < (1ll << 30), "n_tokens = %d not in [0, 2^30 / Hkv)",
+             n_tokens);
+  NOSA_CHECK(k && v && cu_tokens && aligned16(k) && aligned16(v) && aligned16(cu_tokens) && aligned16(start),
+             "k/v/cu_tokens NULL or misaligned");
+  const long long tok = (long long)c.Hkv * c.d;
+  const nosa_kv_strides ns = strides ? *strides : nosa_kv_strides{tok, c.d, tok, c.d};
+  for (int64_t x : {ns.k_tok, ns.k_head, ns.v_tok, ns.v_head})
+    NOSA_CHECK(x >= 0 && x % 8 == 0 && x < (1ll << 40), "stride %lld not a non-negative multiple of 8", (long long)x);
+  NOSA_CHECK(!out || k != v, "k and v are the same rows");
+  if (out)
+    for (int i = 0; i < 2; ++i) {
+      const long long ts = i ? ns.v_tok : ns.k_tok, hs = i ? ns.v_head : ns.k_head;
+      const bool heads = c.Hkv == 1 || hs >= c.d, toks = n_tokens <= 1 || ts >= c.d;
+      const bool nested = c.Hkv == 1 || n_tokens <= 1 || ts >= (c.Hkv - 1) * hs + c.d ||
+                          hs >= (n_tokens - 1) * ts + c.d;
+      NOSA_CHECK(heads && toks && nested, "rows overlap: strides %lld (tokens), %lld (heads)", ts, hs);
+    }
+  a->k = const_cast<uint16_t*>(k);
+  a->v = const_cast<uint16_t*>(v);
+  a->k_tok = ns.k_tok;
+  a->k_head = ns.k_head;
+  a->v_tok = ns.v_tok;
+  a->v_head = ns.v_head;
+  a->n_tokens = n_tokens;
+  a->B = c.B;
+  a->Hkv = c.Hkv;
+  a->cu_tokens = cu_tokens;
+  a->start = start;
+  a->k_pages = reinterpret_cast<uint8_t*>(has_host(st) ? st->host_k : st->k_pool);
+  a->v_pages = reinterpret_cast<uint8_t*>(has_host(st) ? st->host_v : st->v_pool);
+  a->pages_per_group = has_host(st) ? c.max_blocks : c.slots;
+  a->bs = c.block_size;
+  a->max_tokens = c.max_blocks * c.block_size;
+  a->err = st->err;
+  return NOSA_OK;
+}
+
+template <int D>
+nosa_status launch_kv_run(const KvRunArgs& a, bool write, cudaStream_t s) {
+  using R = KvRun<D>;
+  const int grid = (a.n_tokens * a.Hkv + R::ROWS - 1) / R::ROWS;
+  if (grid == 0) return NOSA_OK;
+  if (write) kv4_write_kernel<D><<<grid, R::THREADS, 0, s>>>(a);
+  else kv4_read_kernel<D><<<grid, R::THREADS, 0, s>>>(a);
+  NOSA_CUDA(cudaGetLastError());
+  return NOSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nosa_status nosa_write_kv(const nosa_config* cfg, const nosa_state* st, const uint16_t* k, const uint16_t* v,
+                          const nosa_kv_strides* strides, int32_t n_tokens, const int32_t* cu_tokens,
+                          const int32_t* start, void* stream) {
+  KvRunArgs a;
+  nosa_status r = kv_run_args(cfg, st, k, v, strides, n_tokens, cu_tokens, start, false, &a);
+  if (r != NOSA_OK) return r;
+  return cfg->d == 128 ? launch_kv_run<128>(a, true, as_stream(stream))
+                       : launch_kv_run<64>(a, true, as_stream(stream));
+}
+
+nosa_status nosa_read_kv(const nosa_config* cfg, const nosa_state* st, uint16_t* k, uint16_t* v,
+                         const nosa_kv_strides* strides, int32_t n_tokens, const int32_t* cu_tokens,
+                         const int32_t* start, void* stream) {
+  KvRunArgs a;
+  nosa_status r = kv_run_args(cfg, st, k, v, strides, n_tokens, cu_tokens, start, true, &a);
+  if (r != NOSA_OK) return r;
+  return cfg->d == 128 ? launch_kv_run<128>(a, false, as_stream(stream))
+                       : launch_kv_run<64>(a, false, as_stream(stream));
 }
 
 nosa_status nosa_append(const nosa_config* cfg, const nosa_state* st, const uint16_t* k_new,
@@ -644,10 +784,7 @@ nosa_status nosa_append(const nosa_config* cfg, const nosa_state* st, const uint
   StepArgs a = step_args(c, st);
   a.k_new = k_new;
   a.v_new = v_new;
-  if (c.d == 128) append_kernel<128><<<n_groups(c), 128, 0, as_stream(stream)>>>(a);
-  else append_kernel<64><<<n_groups(c), 128, 0, as_stream(stream)>>>(a);
-  NOSA_CUDA(cudaGetLastError());
-  return NOSA_OK;
+  return launch_append(c, a, as_stream(stream));
 }
 
 nosa_status nosa_score_blocks(const nosa_config* cfg, const nosa_state* st, const uint16_t* rows,
@@ -790,7 +927,7 @@ nosa_status nosa_step_geometry(const nosa_config* cfg, int32_t host_pools, int32
   }
   // K and V pages of one block: 2 x bs x d bf16 values
   const int W = attn_split_for(c.attn_split, k, total, (long long)sms * attn_ctas_per_sm, sms,
-                               4 * c.block_size * c.d, host_pools != 0);
+                               2 * (int)page_bytes(c), host_pools != 0, part_slots(c));
   out->attn_tasks_per_cta = W;
   out->attn_ctas = (total + W - 1) / W;
   return NOSA_OK;
@@ -863,9 +1000,7 @@ nosa_status nosa_attend(const nosa_config* cfg, const nosa_state* st, const uint
   a.k_new = k_new;
   a.v_new = v_new;
   a.ready = ready;
-  if (c.d == 128) append_kernel<128><<<n_groups(c), 128, 0, s>>>(a);
-  else append_kernel<64><<<n_groups(c), 128, 0, s>>>(a);
-  NOSA_CUDA(cudaGetLastError());
+  if ((r = launch_append(c, a, s)) != NOSA_OK) return r;
   // no programmatic early start: the attention reads the length the append just wrote
   return launch_attn(c, st, q, sel, out, ws, s, ready, false);
 }
@@ -954,11 +1089,12 @@ extern "C" nosa_status nosa_decode_attn_noalloc(const nosa_config* cfg, const no
   cudaStream_t s = as_stream(stream);
   // every check (the tensor maps included) before the first work is queued on the stream
   CUtensorMap tk, tv;
-  if ((r = make_pool_maps(c, st, &tk, &tv)) != NOSA_OK) return r;
+  if (!kv4(c) && (r = make_pool_maps(c, st, &tk, &tv)) != NOSA_OK) return r;
   uint32_t* counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + part_bytes);
   // the array keeps the previous call's contents: the last-arriver counters must start at zero
   NOSA_CUDA(cudaMemsetAsync(counters, 0, NG * 4, s));
   const AttnArgs a = attn_args(c, st, q, sel, out, static_cast<float*>(base), counters);
+  if (kv4(c)) return launch_attn_kv4(c, st, a, kPartialSlots, s, /*finest=*/false, /*pdl=*/true);
   return dispatch_attn(c, a, tk, tv, s, /*finest=*/false, /*pdl=*/true);
 }
 

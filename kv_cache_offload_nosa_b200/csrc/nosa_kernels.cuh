@@ -18,6 +18,7 @@
 
 #include <type_traits>
 
+#include "nosa_kv4.cuh"
 #include "nosa_select.cuh"
 
 namespace nosa {
@@ -200,12 +201,71 @@ __device__ void append_token(const StepArgs& a, int gi, int len0) {
   }
 }
 
+// append_token for a 4-bit cache: a warp holds one group of 32 values per lane, so the group's
+// maximum is one warp reduction, and the lanes of a code word put it together by shuffles. The
+// sub-block's mean is over the values that the cache holds. Rows are independent of one another,
+// so nothing of the page is rewritten.
+template <int D>
+__device__ void append_token_kv4(const StepArgs& a, int gi, int len0) {
+  const int pos = len0;
+  const int jb = pos / a.bs, r = pos % a.bs, sb = pos / a.s;
+  int page = a.block_table[(size_t)gi * a.max_blocks + jb];
+  if (page >= a.total_pages || (page < 0 && !a.host_k)) {
+    if (threadIdx.x == 0) set_err(a.err, NOSA_ERR_BLOCK_TABLE);
+    page = -1;
+  }
+  if (threadIdx.x >= D) return;  // whole warps: D is a multiple of 32
+  const int x = threadIdx.x, lane = x & 31, g = x >> 5;
+  const size_t PB = kv4_page_bytes(a.bs, D), hpage = (size_t)gi * a.max_blocks + jb;
+  uint8_t* kp[2] = {page >= 0 ? reinterpret_cast<uint8_t*>(a.k_pool) + page * PB : nullptr,
+                    a.host_k ? reinterpret_cast<uint8_t*>(a.host_k) + hpage * PB : nullptr};
+  uint8_t* vp[2] = {page >= 0 ? reinterpret_cast<uint8_t*>(a.v_pool) + page * PB : nullptr,
+                    a.host_v ? reinterpret_cast<uint8_t*>(a.host_v) + hpage * PB : nullptr};
+  const uint32_t kx = a.k_new[(size_t)gi * D + x], vx = a.v_new[(size_t)gi * D + x];
+  const uint32_t ks = kv4_scale(__reduce_max_sync(0xffffffffu, kx & 0x7fffu));
+  const uint32_t vs = kv4_scale(__reduce_max_sync(0xffffffffu, vx & 0x7fffu));
+  const uint32_t kc = kv4_code(__uint_as_float(kx << 16), kv4_inverse(ks));
+  const uint32_t vc = kv4_code(__uint_as_float(vx << 16), kv4_inverse(vs));
+  uint32_t kw = kc << (4 * (lane & 7)), vw = vc << (4 * (lane & 3));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    kw |= __shfl_xor_sync(0xffffffffu, kw, o);
+    if (o < 4) vw |= __shfl_xor_sync(0xffffffffu, vw, o);
+  }
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    if (!kp[d]) continue;
+    const int s0 = a.bs * (D / 2) + r * (D / 16);
+    if ((lane & 7) == 0)
+      *reinterpret_cast<uint32_t*>(kp[d] + kv4_code_byte<true, D>(r, x)) = kw;
+    if ((lane & 3) == 0)
+      *reinterpret_cast<uint16_t*>(vp[d] + kv4_code_byte<false, D>(r, x)) = static_cast<uint16_t>(vw);
+    if (lane == 0) {
+      reinterpret_cast<uint16_t*>(kp[d] + s0)[g] = static_cast<uint16_t>(ks);
+      reinterpret_cast<uint16_t*>(vp[d] + s0)[g] = static_cast<uint16_t>(vs);
+    }
+  }
+  const int t0 = sb * a.s;
+  float sum = 0.f;
+  if (kp[0] || kp[1]) {
+    const uint8_t* src = kp[0] ? kp[0] : kp[1];
+#pragma unroll 8
+    for (int tau = t0; tau < pos; ++tau) sum += kv4_value<true, D>(src, a.bs, tau - jb * a.bs, x);
+  }
+  sum += (static_cast<float>(kc) - 8.f) * bf16_bits_to_f32(static_cast<uint16_t>(ks));
+  const float mean = __fdiv_rn(sum, (float)(pos - t0 + 1));
+  const size_t ki = ((size_t)gi * a.max_sub + sb) * D + x;
+  if (a.kc16) reinterpret_cast<__nv_bfloat16*>(a.kc)[ki] = __float2bfloat16_rn(mean);
+  else a.kc[ki] = mean;
+}
+
 // VARIANT: the scoring variants (a.mode != 0; 1: mean of the rows, windows; 2: per-row
 // softmax); the chunks leave per-sub-block values in a.units and the group's last CTA turns
 // them into block scores (fused launches only).
 // KC16: kc holds bf16 means (one 16-byte load carries 8 of them; the lanes of a sub-block row
 // still read it in contiguous 128-byte pieces).
-template <int D, bool FUSED, int VARIANT = 0, bool KC16 = false>
+// KV4: the cache holds 4-bit pages; only the append differs.
+template <int D, bool FUSED, int VARIANT = 0, bool KC16 = false, bool KV4 = false>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(StepArgs a) {
   constexpr int LPS = D / 16;        // lanes per sub-block (16 values each)
   constexpr int SPW = 32 / LPS;      // sub-blocks per warp pass
@@ -269,7 +329,8 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(StepArgs a) {
   const int c_app = (FUSED && L > len0) ? (len0 / a.s) / a.chunk : -1;
   const bool parties2 = c_app > 0;  // chunk 0 and another chunk share the publication
   if (FUSED && c == c_app) {
-    append_token<D>(a, gi, len0);
+    if constexpr (KV4) append_token_kv4<D>(a, gi, len0);
+    else append_token<D>(a, gi, len0);
     __syncthreads();
     load_batch(base, icap, va, vb);  // the tail sub-block's mean just changed
   }
@@ -487,7 +548,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(StepArgs a) {
   }
 }
 
-template <int D>
+template <int D, bool KV4 = false>
 __global__ void __launch_bounds__(128) append_kernel(StepArgs a) {
   const int gi = blockIdx.x;
   if (a.ready) {
@@ -501,7 +562,8 @@ __global__ void __launch_bounds__(128) append_kernel(StepArgs a) {
     if (threadIdx.x == 0) set_err(a.err, NOSA_ERR_FULL);
     return;
   }
-  append_token<D>(a, gi, len0);
+  if constexpr (KV4) append_token_kv4<D>(a, gi, len0);
+  else append_token<D>(a, gi, len0);
   __syncthreads();
   if (threadIdx.x == 0) a.seq_len[gi] = len0 + 1;
 }
@@ -721,8 +783,8 @@ __global__ void __launch_bounds__(256) init_tables_kernel(InitArgs a) {
 }
 
 // kc[i] = mean of the present tokens of sub-block i (prefill; fp32, or rounded to bf16 with
-// KC16), zero past the prefill.
-template <int D, bool KC16>
+// KC16), zero past the prefill. KV4: over the values that the 4-bit pages at src hold.
+template <int D, bool KC16, bool KV4 = false>
 __global__ void __launch_bounds__(256) init_kc_kernel(const int32_t* prefill_len, int Hkv,
                                                       const uint16_t* src, int src_pages_per_group,
                                                       float* kc, int max_sub, int bs, int s) {
@@ -736,7 +798,11 @@ __global__ void __launch_bounds__(256) init_kc_kernel(const int32_t* prefill_len
     float sum = 0.f;
     for (int tau = t0; tau < t1; ++tau) {
       const int j = tau / bs, r = tau % bs;
-      sum += bf16_bits_to_f32(src[(((size_t)gi * src_pages_per_group + j) * bs + r) * D + x]);
+      const size_t page = (size_t)gi * src_pages_per_group + j;
+      if constexpr (KV4)
+        sum += kv4_value<true, D>(reinterpret_cast<const uint8_t*>(src) + page * kv4_page_bytes(bs, D), bs, r, x);
+      else
+        sum += bf16_bits_to_f32(src[(page * bs + r) * D + x]);
     }
     const float mean = (t1 > t0) ? __fdiv_rn(sum, (float)(t1 - t0)) : 0.f;
     const size_t ki = ((size_t)gi * max_sub + i) * D + x;
