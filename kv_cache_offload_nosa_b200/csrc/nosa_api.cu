@@ -48,8 +48,13 @@ bool kv4(const nosa_config& c) { return c.kv_bits == 4; }
 size_t page_bytes(const nosa_config& c) {
   return kv4(c) ? (size_t)kv4_page_bytes(c.block_size, c.d) : (size_t)c.block_size * c.d * 2;
 }
-// Partial slots per group of the split-K attention.
-int part_slots(const nosa_config& c) { return kv4(c) ? kPartialSlots : kPartialSlots; }
+// Partial slots per group of the split-K attention. Over 4-bit pages a group may be cut finer when
+// there are few: about 1184 segments (eight a SM) in all, at most 128 a group.
+int part_slots(const nosa_config& c) {
+  if (!kv4(c)) return kPartialSlots;
+  const int want = (1184 + n_groups(c) - 1) / n_groups(c);
+  return want < kPartialSlots ? kPartialSlots : (want > 128 ? 128 : want);
+}
 
 nosa_status check_cfg(const nosa_config* cp) {
   NOSA_CHECK(cp, "cfg is NULL");
@@ -522,30 +527,54 @@ nosa_status dispatch_attn(const nosa_config& c, const AttnArgs& a, const CUtenso
   return launch_attn_t<64, 128>(c, a, tk, tv, s, finest, pdl);
 }
 
-// The same attention over 4-bit pages.
-nosa_status launch_attn_kv4(const nosa_config& c, const nosa_state* st, const AttnArgs& a, int pslots,
-                            cudaStream_t s, bool finest, bool pdl) {
-  AttnKv4Args x;
-  x.a = a;
-  x.k_pages = reinterpret_cast<const uint8_t*>(st->k_pool);
-  x.v_pages = reinterpret_cast<const uint8_t*>(st->v_pool);
-  x.bs = c.block_size;
-  x.pslots = pslots;
-  int dev = 0, sms = 0;
+// The same attention over 4-bit pages. pslots = partial slots per group.
+constexpr int kKv4StageBudget = 72 * 1024;
+
+template <int D, int BS>
+nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t s, bool finest, bool pdl) {
+  using SH = AttnKv4Shape<D, BS>;
+  const int G = x.a.G;
+  int stages = (int)((kKv4StageBudget - SH::smem_bytes(0, G)) / SH::STAGE);
+  stages = stages < 2 ? 2 : (stages > kKv4MaxStages ? kKv4MaxStages : stages);
+  const size_t smem = SH::smem_bytes(stages, G);
+  auto k = attn_kv4_kernel<D, BS>;
+  NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  int dev = 0, sms = 0, per_sm = 0;
   NOSA_CUDA(cudaGetDevice(&dev));
   NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  x.a.W = attn_split_for(c.attn_split, a.k, a.total, 4LL * sms, sms, 2 * (int)page_bytes(c), finest, pslots);
+  NOSA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, SH::THREADS, smem));
+  if (per_sm < 1) per_sm = 1;
+  x.a.W = attn_split_for(c.attn_split, x.a.k, x.a.total, (long long)sms * per_sm, sms, SH::STAGE, finest, x.pslots);
+  x.a.stages = stages;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((a.total + x.a.W - 1) / x.a.W);
-  lc.blockDim = dim3(128);
+  lc.gridDim = dim3((x.a.total + x.a.W - 1) / x.a.W);
+  lc.blockDim = dim3(SH::THREADS);
+  lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = pdl ? 1 : 0;
-  NOSA_CUDA(cudaLaunchKernelEx(&lc, c.d == 128 ? attn_kv4_kernel<128> : attn_kv4_kernel<64>, x));
+  NOSA_CUDA(cudaLaunchKernelEx(&lc, k, x));
   return NOSA_OK;
+}
+
+nosa_status launch_attn_kv4(const nosa_config& c, const nosa_state* st, const AttnArgs& a, int pslots,
+                            cudaStream_t s, bool finest, bool pdl) {
+  AttnKv4Args x;
+  x.a = a;
+  x.k_pages = reinterpret_cast<const uint8_t*>(st->k_pool);
+  x.v_pages = reinterpret_cast<const uint8_t*>(st->v_pool);
+  x.pslots = pslots;
+  if (c.d == 128) {
+    if (c.block_size == 32) return launch_attn_kv4_t<128, 32>(c, x, s, finest, pdl);
+    if (c.block_size == 64) return launch_attn_kv4_t<128, 64>(c, x, s, finest, pdl);
+    return launch_attn_kv4_t<128, 128>(c, x, s, finest, pdl);
+  }
+  if (c.block_size == 32) return launch_attn_kv4_t<64, 32>(c, x, s, finest, pdl);
+  if (c.block_size == 64) return launch_attn_kv4_t<64, 64>(c, x, s, finest, pdl);
+  return launch_attn_kv4_t<64, 128>(c, x, s, finest, pdl);
 }
 
 // ready: per-group flags the attention waits on (and clears), or NULL to wait for the

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(KvRunArgs a) {
         *reinterpret_cast<uint32_t*>(vp + r * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)) = vw;
         if (c < 2)
           *(reinterpret_cast<uint16_t*>((c ? vp : kp) + a.bs * (D / 2) + r * (D / 16)) + g) =
-              static_cast<uint16_t>(scale[c]);
+              static_cast<uint16_t>(c ? scale[1] : scale[0]);
       }
     }
   }
