@@ -528,24 +528,18 @@ nosa_status dispatch_attn(const nosa_config& c, const AttnArgs& a, const CUtenso
 }
 
 // The same attention over 4-bit pages. pslots = partial slots per group.
-constexpr int kKv4StageBudget = 72 * 1024;
-
-template <int D, int BS>
+template <int D, int BS, bool WIDE>
 nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t s, bool finest, bool pdl) {
   using SH = AttnKv4Shape<D, BS>;
-  const int G = x.a.G;
-  int stages = (int)((kKv4StageBudget - SH::smem_bytes(0, G)) / SH::STAGE);
-  stages = stages < 2 ? 2 : (stages > kKv4MaxStages ? kKv4MaxStages : stages);
-  const size_t smem = SH::smem_bytes(stages, G);
-  auto k = attn_kv4_kernel<D, BS>;
-  NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  int dev = 0, sms = 0, per_sm = 0;
+  const size_t smem = SH::smem_bytes(x.a.G);
+  auto k = attn_kv4_kernel<D, BS, WIDE>;
+  int dev = 0, sms = 0;
   NOSA_CUDA(cudaGetDevice(&dev));
   NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  NOSA_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, SH::THREADS, smem));
-  if (per_sm < 1) per_sm = 1;
-  x.a.W = attn_split_for(c.attn_split, x.a.k, x.a.total, (long long)sms * per_sm, sms, SH::STAGE, finest, x.pslots);
-  x.a.stages = stages;
+  NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  x.a.W = attn_split_for(c.attn_split, x.a.k, x.a.total, (long long)sms * SH::ctas_per_sm(x.a.G), sms, SH::STAGE,
+                         finest, x.pslots);
+  x.a.stages = SH::stages(x.a.G);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((x.a.total + x.a.W - 1) / x.a.W);
   lc.blockDim = dim3(SH::THREADS);
@@ -560,6 +554,12 @@ nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t 
   return NOSA_OK;
 }
 
+template <int D, int BS>
+nosa_status launch_attn_kv4_g(const nosa_config& c, const AttnKv4Args& x, cudaStream_t s, bool finest, bool pdl) {
+  return x.a.G > 4 ? launch_attn_kv4_t<D, BS, true>(c, x, s, finest, pdl)
+                   : launch_attn_kv4_t<D, BS, false>(c, x, s, finest, pdl);
+}
+
 nosa_status launch_attn_kv4(const nosa_config& c, const nosa_state* st, const AttnArgs& a, int pslots,
                             cudaStream_t s, bool finest, bool pdl) {
   AttnKv4Args x;
@@ -568,13 +568,13 @@ nosa_status launch_attn_kv4(const nosa_config& c, const nosa_state* st, const At
   x.v_pages = reinterpret_cast<const uint8_t*>(st->v_pool);
   x.pslots = pslots;
   if (c.d == 128) {
-    if (c.block_size == 32) return launch_attn_kv4_t<128, 32>(c, x, s, finest, pdl);
-    if (c.block_size == 64) return launch_attn_kv4_t<128, 64>(c, x, s, finest, pdl);
-    return launch_attn_kv4_t<128, 128>(c, x, s, finest, pdl);
+    if (c.block_size == 32) return launch_attn_kv4_g<128, 32>(c, x, s, finest, pdl);
+    if (c.block_size == 64) return launch_attn_kv4_g<128, 64>(c, x, s, finest, pdl);
+    return launch_attn_kv4_g<128, 128>(c, x, s, finest, pdl);
   }
-  if (c.block_size == 32) return launch_attn_kv4_t<64, 32>(c, x, s, finest, pdl);
-  if (c.block_size == 64) return launch_attn_kv4_t<64, 64>(c, x, s, finest, pdl);
-  return launch_attn_kv4_t<64, 128>(c, x, s, finest, pdl);
+  if (c.block_size == 32) return launch_attn_kv4_g<64, 32>(c, x, s, finest, pdl);
+  if (c.block_size == 64) return launch_attn_kv4_g<64, 64>(c, x, s, finest, pdl);
+  return launch_attn_kv4_g<64, 128>(c, x, s, finest, pdl);
 }
 
 // ready: per-group flags the attention waits on (and clears), or NULL to wait for the

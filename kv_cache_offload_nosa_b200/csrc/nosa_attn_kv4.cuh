@@ -4,8 +4,8 @@
 // the B*Hkv*k (group, selected block) tasks, group after group, are cut in ranges of W, one range
 // per CTA; each range writes one partial (m, l, acc) per query head and group it touches, and the
 // last CTA to finish a group (atomic ticket) merges them. One producer warp brings each task's K
-// and V page (two bulk copies, codes and scales together) into a ring of stages; BS/16 consumer
-// warps own 16 tokens of every page each.
+// and V page (two bulk copies, codes and scales together) into a ring of stages; the consumer warps
+// take 32 tokens each, a page's units going to neighbouring warps and page after page to the next.
 //
 // The pages are never expanded. With s the scales and c the codes,
 //   score:  sum_d q_d K_td = sum_g s_tg sum_{d in g} q_d (c_td - 8),
@@ -18,9 +18,11 @@
 //   V: the same masks or'ed with 1024 (0x6400) give 1024 + c and 1024 + 16 c, and one fp16 FMA
 //      makes c - 8 of either: over a long axis the offset has to go before the sum, which it would
 //      exceed many times.
-// The weights p_t s_tg are split in two fp16 parts (22 bits). They are kept in range for every
-// scale of V: the running reference m is that of x_t + e_t, where e_t is the exponent of the
-// token's largest V scale, and it moves only when a weight would exceed 2^4.
+// The weights p_t s_tg, p_t = 2^(x_t - m), are split in two fp16 parts. They are kept in fp16's
+// range for every scale of V: the reference m is 10 below the largest x_t + e_t seen, where e_t is
+// about the base-2 logarithm of the token's largest V scale, and it moves only when an x_t + e_t
+// exceeds it by more than 13. Weights are thus below 2^15, and one of 2^-14 of the largest still
+// has all 22 bits of its two parts.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -30,7 +32,8 @@
 
 namespace nosa {
 
-constexpr int kKv4MaxStages = 8;
+constexpr int kKv4MaxStages = 16;
+constexpr int kKv4MaxSlots = 128;  // partial slots per group, at most
 
 struct AttnKv4Args {
   AttnArgs a;
@@ -41,13 +44,34 @@ struct AttnKv4Args {
 
 template <int D, int BS>
 struct AttnKv4Shape {
-  static constexpr int NC = BS / 16;
+  static constexpr int NC = 4;             // consumer warps
+  static constexpr int U = BS / 32;        // units of 32 tokens in a page, a warp each
+  static constexpr int STEP = NC / U;      // pages in work at once; the stages are a multiple of it,
+                                           // so that a warp comes to its stages in every round of the
+                                           // ring (a barrier's parity tells one round from the next only)
   static constexpr int THREADS = (NC + 1) * 32;
+  static constexpr int CTAS = D == 128 ? 3 : 4;  // per SM (128 and 96 registers a thread)
   static constexpr int PAGE = kv4_page_bytes(BS, D);
   static constexpr int STAGE = 2 * PAGE;
-  static size_t smem_bytes(int stages, int G) {
-    return 128 + (size_t)stages * STAGE + 2 * kKv4MaxStages * 8 + kKv4MaxStages * sizeof(TaskInfo) + 16 +
-           (size_t)NC * G * (D + 2) * 4;  // alignment, stages, barriers, tasks, flag + barrier, scratch
+  // Shared memory: alignment, barriers, tasks, meeting point, q; what the merges share; the stages.
+  static size_t smem_fixed(int G) {
+    const size_t sums = (size_t)NC * D * 8 * 4, scr = (size_t)NC * G * (D + 2) * 4;
+    const size_t fac = (size_t)G * (kKv4MaxSlots + 2) * 4 + (size_t)NC * G * D * 4;
+    const size_t most = sums > scr ? (sums > fac ? sums : fac) : (scr > fac ? scr : fac);
+    return 128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * (512 + 64) + most;
+  }
+  // As many as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
+  static int stages(int G) {
+    const long long room = 227 * 1024 / CTAS - 1024 - (long long)smem_fixed(G);
+    int n = (int)(room / STAGE);
+    n = n > kKv4MaxStages ? kKv4MaxStages : n;
+    n -= n % STEP;
+    return n < 2 ? 2 : n;
+  }
+  static size_t smem_bytes(int G) { return smem_fixed(G) + (size_t)stages(G) * STAGE; }
+  static int ctas_per_sm(int G) {
+    const int fit = (int)(227 * 1024 / (smem_bytes(G) + 1024));
+    return fit < CTAS ? (fit < 1 ? 1 : fit) : CTAS;
   }
 };
 
@@ -65,6 +89,17 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -74,6 +109,13 @@ __device__ __forceinline__ uint32_t hfma2_u32(uint32_t x, uint32_t m, uint32_t a
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(m), "r"(a));
   return y;
 }
+// (x & m) | o in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(m), "r"(o));
+  return y;
+}
+__device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
 template <int N>
 __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t* w) {
   if constexpr (N == 4) {
@@ -89,10 +131,105 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t* w) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int D, int BS>
-__global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 3) attn_kv4_kernel(AttnKv4Args x) {
+// All warps of a CTA meet: a bounded wait like every other here, so that a warp that has given up on
+// a stage leaves the others an end too. met: the number of meetings before.
+__device__ __forceinline__ bool kv4_meeting(uint64_t* meet, uint32_t met, unsigned long long deadline) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(meet);
+  return __all_sync(0xffffffffu, mbar_wait(meet, met & 1u, deadline));
+}
+
+// The last CTA of a group merges its partials p0 [nseg][G][D + 2] into outg [G][D]; two meetings.
+// Out of line: its loads in flight would cost the main loop registers.
+template <int D, int NC, bool WIDE>
+__device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr, int nseg, int G, uint64_t* meet,
+                               uint32_t met, unsigned long long deadline) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, GE = G * (D + 2);
+  // merge the group's partials: every segment's factor per head, then the weighted sums
+  float* fac = scr;                      // [G][nseg]
+  float* den = scr + G * kKv4MaxSlots;  // [G]
+  for (int h = warp; h < G; h += NC) {
+    float2 ml[kKv4MaxSlots / 32];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kKv4MaxSlots / 32; ++i) {
+      const int sg = 32 * i + lane;
+      ml[i] = sg < nseg ? __ldcg(reinterpret_cast<const float2*>(p0 + (size_t)sg * GE + h * (D + 2)))
+                        : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, ml[i].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int i = 0; i < kKv4MaxSlots / 32; ++i) {
+      const int sg = 32 * i + lane;
+      const float f = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
+      L = fmaf(ml[i].y, f, L);
+      if (sg < nseg) fac[h * nseg + sg] = f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) den[h] = L;
+  }
+  if (!kv4_meeting(meet, met++, deadline)) return false;
+  // a warp takes every NC-th segment, a lane the same columns of all heads
+  constexpr int HG = WIDE ? 8 : 4, CP = D / 64;
+  float2 v[HG][CP];
+#pragma unroll
+  for (int h = 0; h < HG; ++h)
+#pragma unroll
+    for (int c = 0; c < CP; ++c) v[h][c] = make_float2(0.f, 0.f);
+  constexpr int AT = 16 / HG;  // segments in flight
+  for (int sg = warp; sg < nseg; sg += AT * NC) {
+    float2 y[AT][HG][CP];
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+      for (int h = 0; h < HG; ++h)
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+          y[i][h][c] = (sg + i * NC < nseg && h < G)
+                           ? __ldcg(reinterpret_cast<const float2*>(p0 + (size_t)(sg + i * NC) * GE + h * (D + 2) + 2) +
+                                    lane + 32 * c)
+                           : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        const float f = h < G ? fac[h * nseg + min(sg + i * NC, nseg - 1)] : 0.f;
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+          v[h][c].x = fmaf(y[i][h][c].x, f, v[h][c].x);
+          v[h][c].y = fmaf(y[i][h][c].y, f, v[h][c].y);
+        }
+      }
+  }
+  float2* add = reinterpret_cast<float2*>(den + G + (G & 1));  // [NC][G][D / 2]
+#pragma unroll
+  for (int h = 0; h < HG; ++h)
+#pragma unroll
+    for (int c = 0; c < CP; ++c)
+      if (h < G) add[(warp * G + h) * (D / 2) + lane + 32 * c] = v[h][c];
+  if (!kv4_meeting(meet, met++, deadline)) return false;
+  for (int e = tid; e < G * (D / 2); e += NC * 32) {
+    float2 y = add[e];
+#pragma unroll
+    for (int w = 1; w < NC; ++w) {
+      const float2 z = add[w * G * (D / 2) + e];
+      y.x += z.x;
+      y.y += z.y;
+    }
+    const float L = den[e / (D / 2)];
+    reinterpret_cast<float2*>(outg)[e] = L == 0.f ? make_float2(0.f, 0.f) : make_float2(y.x / L, y.y / L);
+  }
+  return true;
+}
+
+// WIDE: more than four query heads a group.
+template <int D, int BS, bool WIDE>
+__global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, BS>::CTAS) attn_kv4_kernel(AttnKv4Args x) {
   using SH = AttnKv4Shape<D, BS>;
-  constexpr int NC = SH::NC;
+  constexpr int NC = SH::NC, U = SH::U;
   constexpr int NG = D / 32;  // groups of a row
   const AttnArgs& a = x.a;
   extern __shared__ uint8_t smem_raw[];
@@ -100,10 +237,13 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 
   const int ST = a.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)ST * SH::STAGE);
   uint64_t* empty = full + kKv4MaxStages;
-  TaskInfo* info = reinterpret_cast<TaskInfo*>(empty + kKv4MaxStages);
+  int2* info = reinterpret_cast<int2*>(empty + kKv4MaxStages);         // a stage's block (-1: none) and length
   uint64_t* meet = reinterpret_cast<uint64_t*>(info + kKv4MaxStages);  // the consumer warps' meeting point
   int* s_flag = reinterpret_cast<int*>(meet + 1);
-  float* scr = reinterpret_cast<float*>(meet + 2);  // [NC][G][D + 2]
+  uint4* sq = reinterpret_cast<uint4*>(meet + 2);              // [NG][32] a lane's q operands of a group
+  float4* sz = reinterpret_cast<float4*>(sq + NG * 32);        // [NG][4] -8 sum q of columns 2 c4, 2 c4 + 1, twice
+  float* scr = reinterpret_cast<float*>(sz + NG * 4);          // [NC][G][D + 2] at a merge
+  float4* sums = reinterpret_cast<float4*>(scr) + warp_id() * NG * 2 * 32;  // this warp's sums, between merges
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int task0 = blockIdx.x * a.W;
@@ -111,7 +251,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], NC);
+      mbar_init(&empty[s], U);
     }
     mbar_init(meet, NC);
     fence_barrier_init();
@@ -128,14 +268,12 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 
     // tasks' pages are looked up at once, lane 0 issues the copies in task order.
     const bool early = a.att_list != nullptr;
     const int32_t* list = early ? a.att_list : a.sel;
-    int it = 0;
+    int it = 0, s = 0, round = 0;  // next task, its stage, and how often the ring has gone round
     bool abort = false;
     for (int sr = 0; sr < ntask && !abort;) {
       const int gi = (task0 + sr) / a.k;
       const int pa = task0 + sr - gi * a.k;
       const int pb = min(task0 + ntask, (gi + 1) * a.k) - gi * a.k;
-      const int first = (int)(((long long)gi * a.k) / a.W);
-      const int lastc = (int)(((long long)gi * a.k + a.k - 1) / a.W);
       sr += pb - pa;
       for (int p = pa; p < pb && !abort;) {
         int pend = pb, L;
@@ -178,104 +316,92 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 
           }
           const int nb = min(32, pend - base);
           __syncwarp();
-          for (int v = 0; v < nb; ++v) {
-            const int j = __shfl_sync(0xffffffffu, j_l, v);
-            const int page = __shfl_sync(0xffffffffu, page_l, v);
-            if (lane == 0) {
-              const int s = it % ST, round = it / ST;
-              if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1, deadline)) {
-                set_err(a.err, NOSA_ERR_TIMEOUT);
-                abort = true;
+          // as many of them at once as there are free stages, a lane each (the first STEP wait)
+          for (int v = 0; v < nb;) {
+            int sl = s + lane, rl = round;  // the stage of task it + lane, for lanes below ST
+            if (sl >= ST) {
+              sl -= ST;
+              ++rl;
+            }
+            bool free = lane < min(ST, nb - v);
+            if (free && rl > 0)
+              free = lane < SH::STEP ? mbar_wait(&empty[sl], (rl - 1) & 1, deadline) : mbar_test(&empty[sl], (rl - 1) & 1);
+            const int n = __ffs(~__ballot_sync(0xffffffffu, free)) - 1;  // (32 of them: ~0 has no bit)
+            const int cnt = n < 0 ? 32 : n;
+            if (cnt == 0) {
+              if (lane == 0) set_err(a.err, NOSA_ERR_TIMEOUT);
+              abort = true;
+              break;
+            }
+            const int j = __shfl_sync(0xffffffffu, j_l, (v + lane) & 31);
+            const int page = __shfl_sync(0xffffffffu, page_l, (v + lane) & 31);
+            if (lane < cnt) {
+              info[sl] = make_int2(j, L);
+              if (j >= 0) {
+                mbar_arrive_expect_tx(&full[sl], SH::STAGE);
+                uint8_t* st = smem + (size_t)sl * SH::STAGE;
+                bulk_load(st, x.k_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[sl]);
+                bulk_load(st + SH::PAGE, x.v_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[sl]);
               } else {
-                TaskInfo ti;
-                ti.gi = gi;
-                ti.j = j;
-                ti.L = L;
-                ti.last = (base + v == pb - 1);
-                ti.seg = blockIdx.x - first;
-                ti.nseg = lastc - first + 1;
-                info[s] = ti;
-                if (j >= 0) {
-                  mbar_arrive_expect_tx(&full[s], SH::STAGE);
-                  uint8_t* st = smem + (size_t)s * SH::STAGE;
-                  bulk_load(st, x.k_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[s]);
-                  bulk_load(st + SH::PAGE, x.v_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[s]);
-                } else {
-                  mbar_arrive(&full[s]);
-                }
-                ++it;
+                mbar_arrive(&full[sl]);
               }
             }
-            abort = __shfl_sync(0xffffffffu, abort, 0);
-            if (abort) break;
+            __syncwarp();
+            v += cnt;
+            it += cnt;
+            s += cnt;
+            if (s >= ST) {
+              s -= ST;
+              ++round;
+            }
           }
         }
         p = pend;
       }
     }
-    if (lane == 0 && !abort) {  // a task with gi < 0 stops the consumers
-      const int s = it % ST, round = it / ST;
-      if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1, deadline)) {
-        set_err(a.err, NOSA_ERR_TIMEOUT);
-      } else {
-        TaskInfo ti = {-1, -1, 0, 0, 0, 0};
-        info[s] = ti;
-        mbar_arrive(&full[s]);
-        ++it;
-      }
-    }
     // never leave the CTA with a copy in flight
-    if (lane == 0)
-      for (int i = max(0, it - ST); i < it; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, deadline);
+    if (lane < min(ST, it)) {
+      const int i = it - 1 - lane;
+      mbar_wait(&full[i % ST], (i / ST) & 1, abort ? globaltimer() + a.wait_ns : deadline);
+    }
     return;
   }
 
   // ---------------------------------------------------------------- consumers
-  // S^T = K . q^T: rows are tokens, columns heads. Row i < 8 of the tile is token (i >> 1) + 4 (i & 1)
-  // and row i + 8 that plus 8: lane c4 of the second product then takes tokens c4, c4 + 4, c4 + 8
-  // and c4 + 12, whose V rows lie in different banks. With G <= 4 column h + 4 repeats head h and
-  // carries the low parts of its weights; with G = 8 the low parts take a second product.
+  // S^T = K . q^T: rows are tokens, columns heads. Row i < 8 of a tile of 16 is token
+  // (i >> 1) + 4 (i & 1) and row i + 8 that plus 8: lane c4 of the second product then takes tokens
+  // c4, c4 + 4, c4 + 8 and c4 + 12, whose V rows lie in different banks. With G <= 4 column h + 4
+  // repeats head h and carries the low parts of its weights; with G = 8 the low parts take a second
+  // product. Columns without a head have q = 0 and are not written.
   const int r = lane >> 2, c4 = lane & 3;
-  const bool wide = a.G > 4;
-  auto col_head = [&](int n) { return wide ? n : (n & 3); };
-  const int h0 = col_head(2 * c4), h1 = col_head(2 * c4 + 1);
-  const bool cv0 = h0 < a.G, cv1 = h1 < a.G;
-  const float lo_sign = (!wide && c4 >= 2) ? -1.f : 0.f;  // low columns take w - fp16(w)
-  const bool owner = wide || c4 < 2;
-  const int tokA = 16 * warp + (r >> 1) + 4 * (r & 1), tokB = tokA + 8;
-  const int tokV = 16 * warp + c4;
-  uint32_t qb[NG][4];
-  float qz[NG][2];
-  float f0 = 0.f, f1 = 0.f;
-  float acc[2 * NG][4];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  int cur = -1;
-  // All consumer warps meet: a bounded wait like every other here, so that a warp that has given
-  // up on a stage leaves the others an end too.
+  auto col_head = [&](int n) { return WIDE ? n : (n & 3); };
+  const float lo_sign = (!WIDE && c4 >= 2) ? -1.f : 0.f;  // low columns take w - fp16(w)
+  const int tok0 = 32 * (warp % U);                       // the unit's first token in its page
+  const int rowA = (r >> 1) + 4 * (r & 1);
+  // K and V row, and scale, of this lane in tile 0 of the unit
+  const uint32_t offK = (tok0 + rowA) * (D / 2) + c4 * (D / 8);
+  const uint32_t offV = SH::PAGE + (tok0 + c4) * (D / 2) + r * (D / 16);
+  const uint32_t offS = BS * (D / 2) + (tok0 + rowA) * (D / 16);
+  constexpr float Y0 = 65536.f + 127.f;  // what x + e is offset by below
   uint32_t met = 0u;
-  auto meeting = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(meet);
-    return mbar_wait(meet, met++ & 1u, deadline);
-  };
+  auto meeting = [&]() -> bool { return kv4_meeting(meet, met++, deadline); };
+  uint32_t kilo = 0x64006400u;  // fp16 (1024, 1024), kept in a register
+  asm volatile("" : "+r"(kilo));
+  int page = warp / U;  // next page of this warp, counted over the CTA's tasks
+  int s = page % ST;
+  uint32_t phase = (page / ST) & 1;
 
-  for (int i = 0;; ++i) {
-    const int s = i % ST;
-    if (!mbar_wait(&full[s], (i / ST) & 1, deadline)) {
-      set_err(a.err, NOSA_ERR_TIMEOUT);
-      break;
-    }
-    const TaskInfo ti = info[s];
-    if (ti.gi < 0) break;
-    const uint8_t* kst = smem + (size_t)s * SH::STAGE;
-    const uint8_t* vst = kst + SH::PAGE;
-    if (ti.gi != cur) {
-      // q as fp16 rows: each head's largest magnitude goes to [2^13, 2^14), so that what the
-      // conversion drops is 2^-38 of it
-      cur = ti.gi;
+  for (int sr = 0; sr < ntask;) {
+    const int gi = (task0 + sr) / a.k;
+    const int pend = min(task0 + ntask, (gi + 1) * a.k) - task0;
+    sr = pend;
+    // q as fp16 rows: each head's largest magnitude goes to [2^13, 2^14), so that what the
+    // conversion drops is 2^-38 of it
+    float f0, f1;
+    {
       const int qhead = col_head(r);
       const bool qok = qhead < a.G;
-      const uint16_t* qrow = a.q + ((size_t)(cur / a.Hkv) * a.Hq + (cur % a.Hkv) * a.G + (qok ? qhead : 0)) * D;
+      const uint16_t* qrow = a.q + ((size_t)(gi / a.Hkv) * a.Hq + (gi % a.Hkv) * a.G + (qok ? qhead : 0)) * D;
       uint4 qv[NG];
       uint32_t mx = 0u;
 #pragma unroll
@@ -290,236 +416,337 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, BS == 128 ? 1 : 
       // 13 - exponent, kept where both it and what undoes it are floats
       const int e = min(max(140 - static_cast<int>(mx >> 7), -100), 100);
       const float up = __uint_as_float((127 + e) << 23), up16 = up * 0.0625f;
-      float zero[NG];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};  // values (0, 1) .. (6, 7)
-        // even codes take q, odd ones a 16th of it; the fragments pair codes i and i + 4
-        qb[g][0] = pack_f16(bf16_lo(w[0]) * up, bf16_lo(w[2]) * up);
-        qb[g][1] = pack_f16(bf16_hi(w[0]) * up16, bf16_hi(w[2]) * up16);
-        qb[g][2] = pack_f16(bf16_lo(w[1]) * up, bf16_lo(w[3]) * up);
-        qb[g][3] = pack_f16(bf16_hi(w[1]) * up16, bf16_hi(w[3]) * up16);
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 q2 = __half22float2(*reinterpret_cast<const __half2*>(&qb[g][j]));
-          z += ((j & 1) ? 16.f : 1.f) * (q2.x + q2.y);
-        }
-        z += __shfl_xor_sync(0xffffffffu, z, 1);
-        z += __shfl_xor_sync(0xffffffffu, z, 2);
-        zero[g] = -8.f * 0x1p-24f * z;
-      }
       const float fq = __uint_as_float((127 - e) << 23) * a.scale_log2 * 0x1p24f;
       // from column r of B (all four c4 lanes agree) to columns 2 c4, 2 c4 + 1 of C
       f0 = __shfl_sync(0xffffffffu, fq, 8 * c4);
       f1 = __shfl_sync(0xffffffffu, fq, 8 * c4 + 4);
+      // warp g leaves group g's operands in shared memory (all of them would take 24 registers)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        qz[g][0] = __shfl_sync(0xffffffffu, zero[g], 8 * c4);
-        qz[g][1] = __shfl_sync(0xffffffffu, zero[g], 8 * c4 + 4);
-      }
+        if (g != warp) continue;
+        const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};  // values (0, 1) .. (6, 7)
+        // even codes take q, odd ones a 16th of it; the fragments pair codes i and i + 4
+        const uint32_t qb[4] = {pack_f16(bf16_lo(w[0]) * up, bf16_lo(w[2]) * up),
+                                pack_f16(bf16_hi(w[0]) * up16, bf16_hi(w[2]) * up16),
+                                pack_f16(bf16_lo(w[1]) * up, bf16_lo(w[3]) * up),
+                                pack_f16(bf16_hi(w[1]) * up16, bf16_hi(w[3]) * up16)};
+        float z = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < 2 * NG; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.f;
-    }
-    const int nval = (ti.j >= 0) ? min(16, ti.L - ti.j * BS - 16 * warp) : 0;
-    if (nval > 0) {
-      // ---- scores
-      uint32_t ka[NG], kb[NG], sk[NG], sv[NG];  // scales: [0, NG/2) row A, [NG/2, NG) row B
-      lds_words<NG>(kst + tokA * (D / 2) + c4 * (D / 8), ka);
-      lds_words<NG>(kst + tokB * (D / 2) + c4 * (D / 8), kb);
-      lds_words<NG / 2>(kst + BS * (D / 2) + tokA * (D / 16), sk);
-      lds_words<NG / 2>(kst + BS * (D / 2) + tokB * (D / 16), sk + NG / 2);
-      lds_words<NG / 2>(vst + BS * (D / 2) + tokA * (D / 16), sv);
-      lds_words<NG / 2>(vst + BS * (D / 2) + tokB * (D / 16), sv + NG / 2);
-      float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float c[4];
-        mma_f16(c, ka[g] & 0x000f000fu, kb[g] & 0x000f000fu, ka[g] & 0x00f000f0u, kb[g] & 0x00f000f0u, qb[g][0],
-                qb[g][1], qz[g][0], qz[g][1], qz[g][0], qz[g][1]);
-        const uint32_t ah = ka[g] >> 8, bh = kb[g] >> 8;
-        mma_f16(c, ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, qb[g][2], qb[g][3], c[0],
-                c[1], c[2], c[3]);
-        const float sA = (g & 1) ? bf16_hi(sk[g / 2]) : bf16_lo(sk[g / 2]);
-        const float sB = (g & 1) ? bf16_hi(sk[NG / 2 + g / 2]) : bf16_lo(sk[NG / 2 + g / 2]);
-        x0 = fmaf(sA, c[0], x0);
-        x1 = fmaf(sA, c[1], x1);
-        x2 = fmaf(sB, c[2], x2);
-        x3 = fmaf(sB, c[3], x3);
-      }
-      const int nA = nval - (tokA - 16 * warp);
-      const bool tA = nA > 0, tB = nA > 8;
-      x0 = (cv0 && tA) ? x0 * f0 : -INFINITY;
-      x1 = (cv1 && tA) ? x1 * f1 : -INFINITY;
-      x2 = (cv0 && tB) ? x2 * f0 : -INFINITY;
-      x3 = (cv1 && tB) ? x3 * f1 : -INFINITY;
-      // rows past the context may hold anything, a NaN scale among it
-#pragma unroll
-      for (int g = 0; g < NG / 2; ++g) {
-        sv[g] = tA ? sv[g] : 0u;
-        sv[NG / 2 + g] = tB ? sv[NG / 2 + g] : 0u;
-      }
-      // exponent of each token's largest V scale (the range keeps 2^-e and sums of it finite)
-      auto top = [&](const uint32_t* w) {
-        uint32_t m = w[0];
-        if constexpr (NG == 4) m = __vmaxu2(m, w[1]);
-        m = max(m & 0xffffu, m >> 16);
-        return static_cast<float>(min(max(static_cast<int>(m >> 7) - 127, -60), 100));
-      };
-      const float eA = top(sv), eB = top(sv + NG / 2);
-      const float y0 = fmaxf(x0 + eA, x2 + eB), y1 = fmaxf(x1 + eA, x3 + eB);
-      if (__any_sync(0xffffffffu, y0 > m0 + 3.f || y1 > m1 + 3.f)) {
-        float mx0 = y0, mx1 = y1;
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        for (int j = 0; j < 4; ++j) {
+          const float2 q2 = __half22float2(*reinterpret_cast<const __half2*>(&qb[j]));
+          z += ((j & 1) ? 16.f : 1.f) * (q2.x + q2.y);
         }
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        const float al0 = mn0 == m0 ? 1.f : ex2(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2(m1 - mn1);
-        m0 = mn0;
-        m1 = mn1;
-        l0 *= al0;
-        l1 *= al1;
-#pragma unroll
-        for (int mt = 0; mt < 2 * NG; ++mt) {
-          acc[mt][0] *= al0;
-          acc[mt][1] *= al1;
-          acc[mt][2] *= al0;
-          acc[mt][3] *= al1;
-        }
-      }
-      const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
-      const float p0 = ex2(x0 - mu0), p1 = ex2(x1 - mu1), p2 = ex2(x2 - mu0), p3 = ex2(x3 - mu1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      // ---- O^T += (c - 8)^T . (p s)^T
-      uint32_t vw[4][NG / 2];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) lds_words<NG / 2>(vst + (tokV + 4 * t) * (D / 2) + r * (D / 16), vw[t]);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float sA = (g & 1) ? bf16_hi(sv[g / 2]) : bf16_lo(sv[g / 2]);
-        const float sB = (g & 1) ? bf16_hi(sv[NG / 2 + g / 2]) : bf16_lo(sv[NG / 2 + g / 2]);
-        const float w0 = p0 * sA, w1 = p1 * sA, w2 = p2 * sB, w3 = p3 * sB;
-        const uint32_t hA = pack_f16(w0, w1), hB = pack_f16(w2, w3);
-        const float2 eA2 = __half22float2(*reinterpret_cast<const __half2*>(&hA));
-        const float2 eB2 = __half22float2(*reinterpret_cast<const __half2*>(&hB));
-        uint32_t b0, b1, d0 = 0u, d1 = 0u;
-        if (wide) {
-          b0 = movmatrix_t(hA);
-          b1 = movmatrix_t(hB);
-          d0 = movmatrix_t(pack_f16(w0 - eA2.x, w1 - eA2.y));
-          d1 = movmatrix_t(pack_f16(w2 - eB2.x, w3 - eB2.y));
-        } else {
-          b0 = movmatrix_t(pack_f16(fmaf(eA2.x, lo_sign, w0), fmaf(eA2.y, lo_sign, w1)));
-          b1 = movmatrix_t(pack_f16(fmaf(eB2.x, lo_sign, w2), fmaf(eB2.y, lo_sign, w3)));
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t sel = 0x4400u + 0x1111u * (2 * (g & 1) + mt);  // byte 2 (g & 1) + mt of both tokens
-          const uint32_t u = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-          const uint32_t v = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-          constexpr uint32_t ONE = 0x3c003c00u, M1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, M72 = 0xd480d480u;
-          const uint32_t a0 = hfma2_u32((u & 0x000f000fu) | 0x64006400u, ONE, M1032);
-          const uint32_t a1 = hfma2_u32((u & 0x00f000f0u) | 0x64006400u, SIXTEENTH, M72);
-          const uint32_t a2 = hfma2_u32((v & 0x000f000fu) | 0x64006400u, ONE, M1032);
-          const uint32_t a3 = hfma2_u32((v & 0x00f000f0u) | 0x64006400u, SIXTEENTH, M72);
-          float* o = acc[2 * g + mt];
-          mma_f16(o, a0, a1, a2, a3, b0, b1, o[0], o[1], o[2], o[3]);
-          if (wide) mma_f16(o, a0, a1, a2, a3, d0, d1, o[0], o[1], o[2], o[3]);
-        }
+        z += __shfl_xor_sync(0xffffffffu, z, 1);
+        z += __shfl_xor_sync(0xffffffffu, z, 2);
+        z *= -8.f * 0x1p-24f;
+        sq[g * 32 + lane] = make_uint4(qb[0], qb[1], qb[2], qb[3]);
+        if (c4 < 2) reinterpret_cast<float*>(sz + g * 4 + (r >> 1))[2 * c4 + (r & 1)] = z;
       }
     }
-    // the stage has been read: hand it back before the merge
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
+    bool ok = meeting();
+    float acc[2 * NG][4];
+#pragma unroll
+    for (int mt = 0; mt < 2 * NG; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+    // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0)
+    float m0 = -INFINITY, m1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool huge = false;
+    // The tensor cores truncate as they add: an error of about 2^-24 a step, all one way. Every
+    // 16 units the accumulators go to sums in shared memory, held relative to (r0, r1).
+    float r0 = -INFINITY, r1 = -INFINITY;
+    int since = 0;
+    auto to_sums = [&](bool first) {
+      const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
+#pragma unroll
+      for (int mt = 0; mt < 2 * NG; ++mt) {
+        float4 v = first ? make_float4(0.f, 0.f, 0.f, 0.f) : sums[mt * 32 + lane];
+        v.x = fmaf(v.x, al0, acc[mt][0]);
+        v.y = fmaf(v.y, al1, acc[mt][1]);
+        v.z = fmaf(v.z, al0, acc[mt][2]);
+        v.w = fmaf(v.w, al1, acc[mt][3]);
+        sums[mt * 32 + lane] = v;
+        acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+      }
+      r0 = m0;
+      r1 = m1;
+    };
+    bool kept = false;
 
-    if (ti.last) {
-      // ------------------------------------------------ flush this group's part
-      float L0 = l0, L1 = l1;
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        L0 += __shfl_xor_sync(0xffffffffu, L0, o);
-        L1 += __shfl_xor_sync(0xffffffffu, L1, o);
-      }
-      if (!wide) {
-#pragma unroll
-        for (int mt = 0; mt < 2 * NG; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][e] += __shfl_xor_sync(0xffffffffu, acc[mt][e], 2);
-      }
-      bool ok = meeting();  // the previous merge has read the scratch
-      if (owner) {
-        float* w0 = scr + ((size_t)warp * a.G + h0) * (D + 2);
-        float* w1 = scr + ((size_t)warp * a.G + h1) * (D + 2);
-        if (r == 0) {
-          if (cv0) w0[0] = m0, w0[1] = L0;
-          if (cv1) w1[0] = m1, w1[1] = L1;
-        }
-        // rows r and r + 8 of tile mt of group g: values 32g + 4r + 2mt and the next
-#pragma unroll
-        for (int mt = 0; mt < 2 * NG; ++mt) {
-          const int at = 2 + 32 * (mt / 2) + 4 * r + 2 * (mt & 1);
-          if (cv0) *reinterpret_cast<float2*>(w0 + at) = make_float2(acc[mt][0], acc[mt][2]);
-          if (cv1) *reinterpret_cast<float2*>(w1 + at) = make_float2(acc[mt][1], acc[mt][3]);
-        }
-      }
-      ok = ok && meeting();
-      const int gi = ti.gi, GE = a.G * (D + 2);
-      float* part = a.partials + ((size_t)gi * x.pslots + ti.seg) * GE;
-      for (int e = tid; e < GE; e += NC * 32) {
-        const int h = e / (D + 2), col = e % (D + 2);
-        float M = -INFINITY;
-        for (int w = 0; w < NC; ++w) M = fmaxf(M, scr[((size_t)w * a.G + h) * (D + 2)]);
-        float v = M;
-        if (col != 0) {
-          v = 0.f;
-          for (int w = 0; w < NC; ++w) {
-            const float* ww = scr + ((size_t)w * a.G + h) * (D + 2);
-            v += ww[col] * (ww[0] == M ? 1.f : ex2(ww[0] - M));
-          }
-        }
-        part[e] = v;
-      }
-      __threadfence();
-      ok = ok && meeting();
-      if (ok && tid == 0) *s_flag = (atomicAdd(&a.counters[gi], 1u) == (unsigned)(ti.nseg - 1));
-      ok = ok && meeting();
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
+    for (; page < pend; page += SH::STEP) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, deadline))) {
         set_err(a.err, NOSA_ERR_TIMEOUT);
-        break;
+        return;
       }
-      if (*s_flag) {
+      const int2 ti = info[s];
+      const uint8_t* st = smem + (size_t)s * SH::STAGE;
+      const int nval = ti.x >= 0 ? ti.y - ti.x * BS - tok0 : 0;
+      if (nval > 0) {
+        // ---- scores of two tiles of 16 tokens: [tile][row A, row B][column]
+        float xs[2][2][2];
+        uint32_t sv[2][2][NG / 2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint32_t ka[NG], kb[NG], sk[2][NG / 2];
+          lds_words<NG>(st + offK + (16 * t) * (D / 2), ka);
+          lds_words<NG>(st + offK + (16 * t + 8) * (D / 2), kb);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            lds_words<NG / 2>(st + offS + (16 * t + 8 * b) * (D / 16), sk[b]);
+            lds_words<NG / 2>(st + SH::PAGE + offS + (16 * t + 8 * b) * (D / 16), sv[t][b]);
+            xs[t][b][0] = xs[t][b][1] = 0.f;
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint4 qb = sq[g * 32 + lane];
+            const float4 qz = sz[g * 4 + c4];
+            float c[4];
+            mma_f16(c, ka[g] & 0x000f000fu, kb[g] & 0x000f000fu, ka[g] & 0x00f000f0u, kb[g] & 0x00f000f0u, qb.x, qb.y,
+                    qz.x, qz.y, qz.z, qz.w);
+            const uint32_t ah = ka[g] >> 8, bh = kb[g] >> 8;
+            mma_f16(c, ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, qb.z, qb.w, c[0], c[1],
+                    c[2], c[3]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float sc = (g & 1) ? bf16_hi(sk[b][g / 2]) : bf16_lo(sk[b][g / 2]);
+              xs[t][b][0] = fmaf(sc, c[2 * b], xs[t][b][0]);
+              xs[t][b][1] = fmaf(sc, c[2 * b + 1], xs[t][b][1]);
+            }
+          }
+        }
+        if (nval < 32) {
+          // rows past the context may hold anything, a NaN scale among it
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              if (16 * t + 8 * b + rowA >= nval) {
+                xs[t][b][0] = xs[t][b][1] = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < NG / 2; ++g) sv[t][b][g] = 0u;
+              }
+        }
+        // The bf16 bits of a scale, as an integer over 128, are its base-2 logarithm plus 127 within
+        // 0.09. 0x4b000000 + bits is 2^23 + bits as a float: over 128 that is Y0 + e. (e is at least
+        // -60, so that 2^-e and sums of it stay finite.)
+        float yn0 = -INFINITY, yn1 = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float top = 0x1p-60f;
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g) top = fmaxf(top, fmaxf(bf16_lo(sv[t][b][g]), bf16_hi(sv[t][b][g])));
+            const float e = 0x1p-7f * __uint_as_float(__byte_perm(__float_as_uint(top), 0x4b000000u, 0x7632));
+            yn0 = fmaxf(yn0, fmaf(xs[t][b][0], f0, e));
+            yn1 = fmaxf(yn1, fmaf(xs[t][b][1], f1, e));
+          }
+        if (__any_sync(0xffffffffu, yn0 > y0 || yn1 > y1)) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            yn0 = fmaxf(yn0, __shfl_xor_sync(0xffffffffu, yn0, o));
+            yn1 = fmaxf(yn1, __shfl_xor_sync(0xffffffffu, yn1, o));
+          }
+          float mn0 = fmaxf(m0, yn0 - (Y0 + 10.f)), mn1 = fmaxf(m1, yn1 - (Y0 + 10.f));
+          y0 = fmaxf(y0, yn0 + 3.f);
+          y1 = fmaxf(y1, yn1 + 3.f);
+          huge = huge || __any_sync(0xffffffffu, fabsf(yn0) > 0x1p20f || fabsf(yn1) > 0x1p20f);
+          if (huge) {
+            // scores so large that a sum with e says little: from here on m is the largest score,
+            // found for every unit
+            mn0 = fmaxf(fmaxf(xs[0][0][0], xs[0][1][0]), fmaxf(xs[1][0][0], xs[1][1][0]));
+            mn1 = fmaxf(fmaxf(xs[0][0][1], xs[0][1][1]), fmaxf(xs[1][0][1], xs[1][1][1]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mn0 = fmaxf(mn0, __shfl_xor_sync(0xffffffffu, mn0, o));
+              mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
+            }
+            mn0 = fmaxf(m0, mn0 * f0);
+            mn1 = fmaxf(m1, mn1 * f1);
+            y0 = y1 = -INFINITY;
+          }
+          const float al0 = mn0 == m0 ? 1.f : ex2(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2(m1 - mn1);
+          m0 = mn0;
+          m1 = mn1;
+          l0 *= al0;
+          l1 *= al1;
+#pragma unroll
+          for (int mt = 0; mt < 2 * NG; ++mt) {
+            acc[mt][0] *= al0;
+            acc[mt][1] *= al1;
+            acc[mt][2] *= al0;
+            acc[mt][3] *= al1;
+          }
+        }
+        const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
+        // ---- O^T += (c - 8)^T . (p s)^T
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2(fmaf(xs[t][0][0], f0, -mu0)), p1 = ex2(fmaf(xs[t][0][1], f1, -mu1));
+          const float p2 = ex2(fmaf(xs[t][1][0], f0, -mu0)), p3 = ex2(fmaf(xs[t][1][1], f1, -mu1));
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          uint32_t vw[4][NG / 2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lds_words<NG / 2>(st + offV + (16 * t + 4 * i) * (D / 2), vw[i]);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float sA = (g & 1) ? bf16_hi(sv[t][0][g / 2]) : bf16_lo(sv[t][0][g / 2]);
+            const float sB = (g & 1) ? bf16_hi(sv[t][1][g / 2]) : bf16_lo(sv[t][1][g / 2]);
+            const float w0 = p0 * sA, w1 = p1 * sA, w2 = p2 * sB, w3 = p3 * sB;
+            const uint32_t hA = pack_f16(w0, w1), hB = pack_f16(w2, w3);
+            const float2 eA2 = __half22float2(*reinterpret_cast<const __half2*>(&hA));
+            const float2 eB2 = __half22float2(*reinterpret_cast<const __half2*>(&hB));
+            uint32_t b0, b1, d0 = 0u, d1 = 0u;
+            if constexpr (WIDE) {
+              b0 = movmatrix_t(hA);
+              b1 = movmatrix_t(hB);
+              d0 = movmatrix_t(pack_f16(w0 - eA2.x, w1 - eA2.y));
+              d1 = movmatrix_t(pack_f16(w2 - eB2.x, w3 - eB2.y));
+            } else {
+              b0 = movmatrix_t(pack_f16(fmaf(eA2.x, lo_sign, w0), fmaf(eA2.y, lo_sign, w1)));
+              b1 = movmatrix_t(pack_f16(fmaf(eB2.x, lo_sign, w2), fmaf(eB2.y, lo_sign, w3)));
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint32_t sel = 0x4400u + 0x1111u * (2 * (g & 1) + mt);  // byte 2 (g & 1) + mt of both tokens
+              const uint32_t u = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+              const uint32_t v = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+              constexpr uint32_t ONE = 0x3c003c00u, M1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, M72 = 0xd480d480u;
+              const uint32_t a0 = hfma2_u32(and_or(u, 0x000f000fu, kilo), ONE, M1032);
+              const uint32_t a1 = hfma2_u32(and_or(u, 0x00f000f0u, kilo), SIXTEENTH, M72);
+              const uint32_t a2 = hfma2_u32(and_or(v, 0x000f000fu, kilo), ONE, M1032);
+              const uint32_t a3 = hfma2_u32(and_or(v, 0x00f000f0u, kilo), SIXTEENTH, M72);
+              float* o = acc[2 * g + mt];
+              mma_f16(o, a0, a1, a2, a3, b0, b1, o[0], o[1], o[2], o[3]);
+              if constexpr (WIDE) mma_f16(o, a0, a1, a2, a3, d0, d1, o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      if (++since == 16) {
+        to_sums(!kept);
+        kept = true;
+        since = 0;
+      }
+      s += SH::STEP;
+      if (s >= ST) {
+        s -= ST;
+        phase ^= 1u;
+      }
+    }
+
+    // -------------------------------------------------- this CTA's part of the group
+    if (kept) {
+      const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
+#pragma unroll
+      for (int mt = 0; mt < 2 * NG; ++mt) {
+        const float4 v = sums[mt * 32 + lane];
+        acc[mt][0] = fmaf(v.x, al0, acc[mt][0]);
+        acc[mt][1] = fmaf(v.y, al1, acc[mt][1]);
+        acc[mt][2] = fmaf(v.z, al0, acc[mt][2]);
+        acc[mt][3] = fmaf(v.w, al1, acc[mt][3]);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int mt = 0; mt < 2 * NG; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] += __shfl_xor_sync(0xffffffffu, acc[mt][e], 2);
+    }
+    ok = meeting() && ok;  // everyone has read q and its sums
+    if (WIDE || c4 < 2) {
+      const int h0 = col_head(2 * c4), h1 = col_head(2 * c4 + 1);
+      const bool cv0 = h0 < a.G, cv1 = h1 < a.G;
+      float* w0 = scr + ((size_t)warp * a.G + h0) * (D + 2);
+      float* w1 = scr + ((size_t)warp * a.G + h1) * (D + 2);
+      if (r == 0) {
+        if (cv0) w0[0] = m0, w0[1] = l0;
+        if (cv1) w1[0] = m1, w1[1] = l1;
+      }
+      // rows r and r + 8 of tile mt of group g: values 32g + 4r + 2mt and the next
+#pragma unroll
+      for (int mt = 0; mt < 2 * NG; ++mt) {
+        const int at = 2 + 32 * (mt / 2) + 4 * r + 2 * (mt & 1);
+        if (cv0) *reinterpret_cast<float2*>(w0 + at) = make_float2(acc[mt][0], acc[mt][2]);
+        if (cv1) *reinterpret_cast<float2*>(w1 + at) = make_float2(acc[mt][1], acc[mt][3]);
+      }
+    }
+    if (!ok || !meeting()) {
+      set_err(a.err, NOSA_ERR_TIMEOUT);
+      return;
+    }
+    const int first = (int)(((long long)gi * a.k) / a.W);
+    const int nseg = (int)(((long long)gi * a.k + a.k - 1) / a.W) - first + 1, seg = blockIdx.x - first;
+    const int GE = a.G * (D + 2);
+    float* outg = a.out + ((size_t)(gi / a.Hkv) * a.Hq + (gi % a.Hkv) * a.G) * D;  // [G][D]
+    {
+      // two values of a head per thread: the warps' parts, to the group's partial slot, or to the
+      // output where this CTA has the whole group
+      float* part = a.partials + ((size_t)gi * x.pslots + seg) * GE;
+      for (int e = tid; e < a.G * (D / 2); e += NC * 32) {
+        const int h = e / (D / 2), col = 2 * (e % (D / 2));
+        float M = -INFINITY, f[NC], L = 0.f;
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NC; ++w) {
+          f[w] = scr[(w * a.G + h) * (D + 2)];
+          M = fmaxf(M, f[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < NC; ++w) {
+          const float* ww = scr + (w * a.G + h) * (D + 2);
+          f[w] = f[w] == M ? 1.f : ex2(f[w] - M);
+          const float2 y = *reinterpret_cast<const float2*>(ww + 2 + col);
+          L = fmaf(ww[1], f[w], L);
+          v.x = fmaf(y.x, f[w], v.x);
+          v.y = fmaf(y.y, f[w], v.y);
+        }
+        if (nseg == 1) {
+          *reinterpret_cast<float2*>(outg + h * D + col) =
+              L == 0.f ? make_float2(0.f, 0.f) : make_float2(v.x / L, v.y / L);
+        } else {
+          *reinterpret_cast<float2*>(part + h * (D + 2) + 2 + col) = v;
+          if (col == 0) *reinterpret_cast<float2*>(part + h * (D + 2)) = make_float2(M, L);
+        }
+      }
+    }
+    bool last = true;
+    if (nseg > 1) {
+      __threadfence();
+      ok = meeting();
+      if (ok && tid == 0) *s_flag = (atomicAdd(&a.counters[gi], 1u) == (unsigned)(nseg - 1));
+      if (!ok || !meeting()) {
+        set_err(a.err, NOSA_ERR_TIMEOUT);
+        return;
+      }
+      last = *s_flag != 0;
+      if (last) {
         __threadfence();
-        const float* p0 = a.partials + (size_t)gi * x.pslots * GE;
-        const int b = gi / a.Hkv, g = gi % a.Hkv;
-        for (int e = tid; e < a.G * D; e += NC * 32) {
-          const int h = e / D, col = e % D;
-          float M = -INFINITY;
-          for (int sg = 0; sg < ti.nseg; ++sg) M = fmaxf(M, __ldcg(p0 + (size_t)sg * GE + h * (D + 2)));
-          float num = 0.f, den = 0.f;
-          for (int sg = 0; sg < ti.nseg; ++sg) {
-            const float* ps = p0 + (size_t)sg * GE + h * (D + 2);
-            const float m = __ldcg(ps), f = m == M ? 1.f : ex2(m - M);
-            den += __ldcg(ps + 1) * f;
-            num += __ldcg(ps + 2 + col) * f;
-          }
-          a.out[((size_t)b * a.Hq + g * a.G + h) * D + col] = den == 0.f ? 0.f : num / den;
+        if (!kv4_merge<D, NC, WIDE>(a.partials + (size_t)gi * x.pslots * GE, outg, scr, nseg, a.G, meet, met, deadline)) {
+          set_err(a.err, NOSA_ERR_TIMEOUT);
+          return;
         }
-        if (tid == 0) {
-          a.counters[gi] = 0u;
-          if (flags) a.sel_flag[(size_t)gi * kFlagStride] = 0u;  // every CTA of the group passed its wait
-          if (a.e_flag) {
-            a.e_flag[(size_t)gi * kFlagStride] = 0u;
-            a.e_flag[(size_t)gi * kFlagStride + 3] = 0u;
-          }
-        }
+        met += 2u;
+        if (tid == 0) a.counters[gi] = 0u;
       }
-      cur = -1;
+    }
+    // the scratch turns into sums again once everyone is done with it
+    if (sr < ntask && !meeting()) {
+      set_err(a.err, NOSA_ERR_TIMEOUT);
+      return;
+    }
+    if (last && tid == 0) {
+      if (flags) a.sel_flag[(size_t)gi * kFlagStride] = 0u;  // every CTA of the group passed its wait
+      if (a.e_flag) {
+        a.e_flag[(size_t)gi * kFlagStride] = 0u;
+        a.e_flag[(size_t)gi * kFlagStride + 3] = 0u;
+      }
     }
   }
 }
