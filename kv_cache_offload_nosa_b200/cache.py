@@ -36,19 +36,21 @@ def run_strides(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor,
                 device: torch.device) -> nosa_kv_strides:
     """Strides of a run's K and V rows; refuses (NosaError, NOSA_EINVAL) tensors that are not
     [n_tokens, Hkv, d] of 16-bit values on `device` with contiguous rows."""
+    want = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d)
+    strides = []
     for name, t in (("k", k), ("v", v)):
-        if not t.is_cuda or t.device != device:
+        if t.device != device:
             raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
-        if t.dtype not in (torch.bfloat16, torch.int16):
+        if t.dtype is not torch.bfloat16 and t.dtype is not torch.int16:
             raise NosaError(NOSA_EINVAL, f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
-        if t.dim() != 3 or tuple(t.shape[1:]) != (cfg.Hkv, cfg.d) or t.shape[0] != k.shape[0]:
-            raise NosaError(NOSA_EINVAL, f"{name} must be [n_tokens, {cfg.Hkv}, {cfg.d}], not {tuple(t.shape)}")
-        if t.stride(2) != 1:
+        if t.shape != want:
+            raise NosaError(NOSA_EINVAL, f"{name} must be {list(want)}, not {list(t.shape)}")
+        tok, head, value = t.stride()
+        if value != 1:
             raise NosaError(NOSA_EINVAL, f"{name}'s rows must be contiguous")
-    # the stride of a dimension of size 1 says nothing
-    at = [s for t in (k, v) for s in (t.stride(0) if t.shape[0] > 1 else cfg.Hkv * cfg.d,
-                                      t.stride(1) if cfg.Hkv > 1 else cfg.d)]
-    return nosa_kv_strides(*at)
+        # the stride of a dimension of size 1 says nothing
+        strides += [tok if want[0] > 1 else want[1] * want[2], head if want[1] > 1 else want[2]]
+    return nosa_kv_strides(*strides)
 
 
 def check_int32(**bufs):

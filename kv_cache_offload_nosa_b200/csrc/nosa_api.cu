@@ -384,10 +384,8 @@ nosa_status make_pool_map(CUtensorMap* m, const nosa_config& c, void* pool) {
 // Tasks ((group, block) pairs) per attention CTA. split > 0: the caller's width; finest: the
 // smallest width the partial slots allow; otherwise the automatic rule below. target = the
 // resident attention CTAs (SMs x CTAs per SM), stage = bytes of one block's K and V pages.
-// slots = the partial slots per group.
-int attn_split_for(int split, int k, int total, long long target, int sms, int stage, bool finest,
-                   int slots = kPartialSlots) {
-  const int wmin = (k + slots - 2) / (slots - 1);
+int attn_split_for(int split, int k, int total, long long target, int sms, int stage, bool finest) {
+  const int wmin = (k + kPartialSlots - 2) / (kPartialSlots - 1);
   int W = split;
   if (W <= 0 && finest) W = wmin;
   if (W <= 0) {
@@ -414,6 +412,18 @@ int attn_split_for(int split, int k, int total, long long target, int sms, int s
   if (W < wmin) W = wmin;
   if (W < 1) W = 1;
   return W;
+}
+
+// The same for 4-bit pages: equal ranges, one for each CTA that the GPU holds at once, wherever
+// they cut a group. Unpacking bounds the kernel and CTAs share an SM's issue slots, so an even load
+// counts for more than whole groups (2048 blocks of 32 groups, 444 CTAs at once: 144 us with
+// W = 148, 172 us with the divisor 128; 64 blocks of 128 groups: 31 us with either 19 or 32).
+// finest: as above, up to the 16 parts that a group has there.
+int attn_split_kv4(int split, int k, int total, long long target, bool finest, int slots) {
+  auto width = [&](int parts) { return (k + parts - 2) / (parts - 1); };  // a group in `parts` ranges at most
+  const int W = split > 0 ? split : finest ? width(kPartialSlots) : (int)((total + target - 1) / target);
+  const int least = width(slots);
+  return W < least ? least : (W < 1 ? 1 : W);
 }
 
 // finest: the smallest split width the partial slots allow (used when the attention of each
@@ -537,8 +547,7 @@ nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t 
   NOSA_CUDA(cudaGetDevice(&dev));
   NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  x.a.W = attn_split_for(c.attn_split, x.a.k, x.a.total, (long long)sms * SH::ctas_per_sm(x.a.G), sms, SH::STAGE,
-                         finest, x.pslots);
+  x.a.W = attn_split_kv4(c.attn_split, x.a.k, x.a.total, (long long)sms * SH::ctas_per_sm(x.a.G), finest, x.pslots);
   x.a.stages = SH::stages(x.a.G);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((x.a.total + x.a.W - 1) / x.a.W);
@@ -771,7 +780,7 @@ nosa_status kv_run_args(const nosa_config* cfg, const nosa_state* st, const uint
 template <int D>
 nosa_status launch_kv_run(const KvRunArgs& a, bool write, cudaStream_t s) {
   using R = KvRun<D>;
-  const int grid = (a.n_tokens * a.Hkv + R::ROWS - 1) / R::ROWS;
+  const int grid = (a.n_tokens + R::TOKENS - 1) / R::TOKENS * a.Hkv;
   if (grid == 0) return NOSA_OK;
   if (write) kv4_write_kernel<D><<<grid, R::THREADS, 0, s>>>(a);
   else kv4_read_kernel<D><<<grid, R::THREADS, 0, s>>>(a);
@@ -955,8 +964,9 @@ nosa_status nosa_step_geometry(const nosa_config* cfg, int32_t host_pools, int32
     return NOSA_OK;
   }
   // K and V pages of one block: 2 x bs x d bf16 values
-  const int W = attn_split_for(c.attn_split, k, total, (long long)sms * attn_ctas_per_sm, sms,
-                               2 * (int)page_bytes(c), host_pools != 0, part_slots(c));
+  const long long at_once = (long long)sms * attn_ctas_per_sm;
+  const int W = kv4(c) ? attn_split_kv4(c.attn_split, k, total, at_once, host_pools != 0, part_slots(c))
+                       : attn_split_for(c.attn_split, k, total, at_once, sms, 4 * c.block_size * c.d, host_pools != 0);
   out->attn_tasks_per_cta = W;
   out->attn_ctas = (total + W - 1) / W;
   return NOSA_OK;

@@ -38,7 +38,9 @@ __device__ __forceinline__ uint32_t kv4_scale(uint32_t amax) {
 }
 // The multiplier that takes a value to its code minus 8.
 __device__ __forceinline__ float kv4_inverse(uint32_t scale) {
-  return (scale == 0u || scale == 0x7fffu) ? 0.f : __frcp_rn(__uint_as_float(scale << 16)) * (1.0f + 0x1p-20f);
+  float r;  // within 2^-23 (s is normal, at least 2^-126, and its reciprocal at least 2^-125)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float(scale << 16)));
+  return scale == 0u ? 0.f : r * (1.0f + 0x1p-20f);
 }
 // 0x4b400000 + code: the sum's last place is 1, so its low bits are the rounded integer.
 __device__ __forceinline__ uint32_t kv4_code(float x, float inv) {
@@ -73,101 +75,125 @@ struct KvRunArgs {
   uint32_t* err;
 };
 
-// The tokens that one CTA's rows cover: their sequence and position, found by binary search in
-// cu_tokens. pos < 0: the token belongs to no sequence, or its position is not in the cache.
+// A CTA takes TOKENS tokens of one KV head (the heads of the same tokens are neighbouring CTAs, so
+// that a token-major row is read by CTAs that run together), a thread 8 values of K and of V.
 template <int D>
 struct KvRun {
-  static constexpr int TPR = D / 8;            // threads per row, 8 values each
+  static constexpr int TPR = D / 8;            // threads per row
   static constexpr int THREADS = 256;
   static constexpr int RPP = THREADS / TPR;    // rows per pass
   static constexpr int U = 4;                  // passes, all in flight at once
-  static constexpr int ROWS = RPP * U;
-  static constexpr int TOKENS = ROWS + 1;      // tokens that ROWS rows can touch
+  static constexpr int TOKENS = RPP * U;
 };
 
+// Sequences whose bounds are kept in shared memory; past them the search reads cu_tokens itself.
+constexpr int kKvRunSeqs = 256;
+
+// Page (of its pool, -1: none) and row of every token of the CTA: its sequence by binary search in
+// cu_tokens. A token of no sequence, or with a position outside the cache, has none.
 template <int D>
-__device__ __forceinline__ void kv_run_places(const KvRunArgs& a, int t0, int nt, int2* place) {
-  for (int i = threadIdx.x; i < nt; i += blockDim.x) {
+__device__ __forceinline__ void kv_run_places(const KvRunArgs& a, int t0, int h, int2* place) {
+  __shared__ int cu_s[kKvRunSeqs + 1], start_s[kKvRunSeqs];
+  const bool small = a.B <= kKvRunSeqs;
+  if (small) {
+    for (int i = threadIdx.x; i <= a.B; i += blockDim.x) {
+      cu_s[i] = a.cu_tokens[i];
+      if (i < a.B) start_s[i] = a.start ? a.start[i] : 0;
+    }
+    __syncthreads();
+  }
+  const int shift = 31 - __clz(a.bs);  // bs is a power of two
+  for (int i = threadIdx.x; i < KvRun<D>::TOKENS; i += blockDim.x) {
     const int t = t0 + i;
     int lo = 0, hi = a.B - 1;  // the last b with cu_tokens[b] <= t, if any
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.cu_tokens[mid] <= t) lo = mid;
+      if ((small ? cu_s[mid] : a.cu_tokens[mid]) <= t) lo = mid;
       else hi = mid - 1;
     }
-    int pos = -1;
-    const int c0 = a.cu_tokens[lo];
-    if (t >= c0 && t < a.cu_tokens[lo + 1]) {
-      const long long p = (long long)(a.start ? a.start[lo] : 0) + (t - c0);
-      if (p >= 0 && p < a.max_tokens) pos = static_cast<int>(p);
-      else set_err(a.err, NOSA_ERR_FULL);
+    int2 at = make_int2(-1, 0);
+    const int c0 = small ? cu_s[lo] : a.cu_tokens[lo], c1 = small ? cu_s[lo + 1] : a.cu_tokens[lo + 1];
+    if (t >= c0 && t < c1 && t < a.n_tokens) {
+      const long long p = (long long)(small ? start_s[lo] : a.start ? a.start[lo] : 0) + (t - c0);
+      if (p >= 0 && p < a.max_tokens)
+        at = make_int2((lo * a.Hkv + h) * a.pages_per_group + (static_cast<int>(p) >> shift),
+                       static_cast<int>(p) & (a.bs - 1));
+      else
+        set_err(a.err, NOSA_ERR_FULL);
     }
-    place[i] = make_int2(lo, pos);
+    place[i] = at;
   }
+  __syncthreads();
 }
 
-// Writes K and V rows into their pages: one thread takes 8 values of K and of V, four threads a
-// group (its maximum by two shuffles). Bound by memory: 2 bytes in and 9/16 out a value.
+__device__ __forceinline__ uint32_t max_abs_bf162(uint32_t x, uint32_t y) {  // per half, NaN if either is
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The code word of 8 values (pairs of consecutive ones) and the scale of their group, whose other
+// values the three neighbouring lanes hold. A code is the low bits of 0x4b400000 + code; the words
+// of eight add up in base 16, and their constant parts to a constant.
+__device__ __forceinline__ uint32_t kv4_pack(uint4 x, uint32_t* scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = max_abs_bf162(max_abs_bf162(w[0], w[1]), max_abs_bf162(w[2], w[3]));
+  m = max_abs_bf162(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_abs_bf162(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = max_abs_bf162(m, __byte_perm(m, m, 0x1032));
+  *scale = kv4_scale(m & 0xffffu);
+  const float inv = kv4_inverse(*scale);
+  uint32_t word = 0u;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const float v = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    word = word * 16u + __float_as_uint(fmaf(v, inv, 12582912.f + 8.f));
+  }
+  constexpr uint32_t BASE = 0x4b400000u * 0x11111111u;
+  return word - BASE;
+}
+
+// Writes K and V rows into their pages. Bound by issue slots before memory in its first form (83 %
+// of them at 3.2 TB/s); see KvRun for the mapping that took the index arithmetic out of the rows.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_write_kernel(KvRunArgs a) {
   using R = KvRun<D>;
   __shared__ int2 place[R::TOKENS];
-  const int row0 = blockIdx.x * R::ROWS, rows = a.n_tokens * a.Hkv;  // below 2^31
-  const int t0 = row0 / a.Hkv;
-  const int sub = threadIdx.x % R::TPR, g = sub >> 2, c = sub & 3;
+  const int h = blockIdx.x % a.Hkv, t0 = blockIdx.x / a.Hkv * R::TOKENS;
+  const int i0 = threadIdx.x / R::TPR, sub = threadIdx.x % R::TPR, g = sub >> 2, c = sub & 3;
   uint4 kx[R::U], vx[R::U];
+  {
+    const uint16_t* kr = a.k + (size_t)(t0 + i0) * a.k_tok + (size_t)h * a.k_head + 8 * sub;
+    const uint16_t* vr = a.v + (size_t)(t0 + i0) * a.v_tok + (size_t)h * a.v_head + 8 * sub;
 #pragma unroll
-  for (int u = 0; u < R::U; ++u) {
-    const int row = row0 + u * R::RPP + threadIdx.x / R::TPR;
-    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int t = row / a.Hkv, h = row % a.Hkv;
-      kx[u] = __ldcs(reinterpret_cast<const uint4*>(a.k + t * a.k_tok + h * a.k_head) + sub);
-      vx[u] = __ldcs(reinterpret_cast<const uint4*>(a.v + t * a.v_tok + h * a.v_head) + sub);
+    for (int u = 0; u < R::U; ++u) {
+      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+      if (t0 + i0 + u * R::RPP < a.n_tokens) {
+        kx[u] = __ldcs(reinterpret_cast<const uint4*>(kr + u * (size_t)R::RPP * a.k_tok));
+        vx[u] = __ldcs(reinterpret_cast<const uint4*>(vr + u * (size_t)R::RPP * a.v_tok));
+      }
     }
   }
-  const int last = min(row0 + R::ROWS, rows) - 1;
-  kv_run_places<D>(a, t0, last / a.Hkv - t0 + 1, place);
-  __syncthreads();
+  kv_run_places<D>(a, t0, h, place);
+  const size_t PB = kv4_page_bytes(a.bs, D);
+  const bool odd = g & 1;
 #pragma unroll
   for (int u = 0; u < R::U; ++u) {
-    const int row = row0 + u * R::RPP + threadIdx.x / R::TPR;
-    uint32_t word[2], scale[2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint4 x = kv ? vx[u] : kx[u];
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                            __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-      m = max(m & 0xffffu, m >> 16);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      scale[kv] = kv4_scale(m);
-      const float inv = kv4_inverse(scale[kv]);
-      word[kv] = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        word[kv] |= (kv4_code(__uint_as_float(w[i] << 16), inv) |
-                     (kv4_code(__uint_as_float(w[i] & 0xffff0000u), inv) << 4)) << (8 * i);
-    }
+    uint32_t ks, vs;
+    const uint32_t kw = kv4_pack(kx[u], &ks), w = kv4_pack(vx[u], &vs);
     // V: this thread's values are the words of r = 2c (low half) and r = 2c + 1 of group g; the
     // thread of the other group of a pair takes one of them, so that each stores 4 bytes
-    const bool odd = g & 1;
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? word[1] & 0xffffu : word[1] >> 16, 4);
-    const uint32_t vw = odd ? (got | (word[1] & 0xffff0000u)) : ((word[1] & 0xffffu) | (got << 16));
-    if (row < rows) {
-      const int2 p = place[row / a.Hkv - t0];
-      if (p.y >= 0) {
-        const int h = row % a.Hkv, r = p.y % a.bs;
-        const size_t at = ((size_t)(p.x * a.Hkv + h) * a.pages_per_group + p.y / a.bs) * kv4_page_bytes(a.bs, D);
-        uint8_t* kp = a.k_pages + at;
-        uint8_t* vp = a.v_pages + at;
-        *reinterpret_cast<uint32_t*>(kp + r * (D / 2) + c * (D / 8) + 4 * g) = word[0];
-        *reinterpret_cast<uint32_t*>(vp + r * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)) = vw;
-        if (c < 2)
-          *(reinterpret_cast<uint16_t*>((c ? vp : kp) + a.bs * (D / 2) + r * (D / 16)) + g) =
-              static_cast<uint16_t>(c ? scale[1] : scale[0]);
-      }
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, 4);
+    const uint32_t vw = odd ? __byte_perm(got, w, 0x7610) : __byte_perm(w, got, 0x5410);
+    const int2 at = place[i0 + u * R::RPP];
+    if (at.x >= 0) {
+      uint8_t* kp = a.k_pages + at.x * PB;
+      uint8_t* vp = a.v_pages + at.x * PB;
+      *reinterpret_cast<uint32_t*>(kp + at.y * (D / 2) + c * (D / 8) + 4 * g) = kw;
+      *reinterpret_cast<uint32_t*>(vp + at.y * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)) = vw;
+      if (c < 2)
+        *(reinterpret_cast<uint16_t*>((c ? vp : kp) + a.bs * (D / 2) + at.y * (D / 16)) + g) =
+            static_cast<uint16_t>(c ? vs : ks);
     }
   }
 }
@@ -194,44 +220,37 @@ template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(KvRunArgs a) {
   using R = KvRun<D>;
   __shared__ int2 place[R::TOKENS];
-  const int row0 = blockIdx.x * R::ROWS, rows = a.n_tokens * a.Hkv;  // below 2^31
-  const int t0 = row0 / a.Hkv;
-  const int sub = threadIdx.x % R::TPR, g = sub >> 2, c = sub & 3;
+  const int h = blockIdx.x % a.Hkv, t0 = blockIdx.x / a.Hkv * R::TOKENS;
+  const int i0 = threadIdx.x / R::TPR, sub = threadIdx.x % R::TPR, g = sub >> 2, c = sub & 3;
   const bool odd = g & 1;
-  const int last = min(row0 + R::ROWS, rows) - 1;
-  kv_run_places<D>(a, t0, last / a.Hkv - t0 + 1, place);
-  __syncthreads();
+  kv_run_places<D>(a, t0, h, place);
+  const size_t PB = kv4_page_bytes(a.bs, D);
   uint32_t kw[R::U], vw[R::U], ks[R::U], vs[R::U];
+  bool any[R::U];
 #pragma unroll
   for (int u = 0; u < R::U; ++u) {
-    const int row = row0 + u * R::RPP + threadIdx.x / R::TPR;
     kw[u] = vw[u] = ks[u] = vs[u] = 0u;
-    if (row < rows) {
-      const int2 p = place[row / a.Hkv - t0];
-      if (p.y >= 0) {
-        const int h = row % a.Hkv, r = p.y % a.bs;
-        const size_t at = ((size_t)(p.x * a.Hkv + h) * a.pages_per_group + p.y / a.bs) * kv4_page_bytes(a.bs, D);
-        const uint8_t* kp = a.k_pages + at;
-        const uint8_t* vp = a.v_pages + at;
-        kw[u] = __ldcs(reinterpret_cast<const uint32_t*>(kp + r * (D / 2) + c * (D / 8) + 4 * g));
-        vw[u] = __ldcs(reinterpret_cast<const uint32_t*>(vp + r * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)));
-        ks[u] = __ldcs(reinterpret_cast<const uint16_t*>(kp + a.bs * (D / 2) + r * (D / 16)) + g);
-        vs[u] = __ldcs(reinterpret_cast<const uint16_t*>(vp + a.bs * (D / 2) + r * (D / 16)) + g);
-      }
+    const int2 at = place[i0 + u * R::RPP];
+    any[u] = at.x >= 0;
+    if (any[u]) {
+      const uint8_t* kp = a.k_pages + at.x * PB;
+      const uint8_t* vp = a.v_pages + at.x * PB;
+      kw[u] = __ldcs(reinterpret_cast<const uint32_t*>(kp + at.y * (D / 2) + c * (D / 8) + 4 * g));
+      vw[u] = __ldcs(reinterpret_cast<const uint32_t*>(vp + at.y * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)));
+      ks[u] = __ldcs(reinterpret_cast<const uint16_t*>(kp + a.bs * (D / 2) + at.y * (D / 16)) + g);
+      vs[u] = __ldcs(reinterpret_cast<const uint16_t*>(vp + a.bs * (D / 2) + at.y * (D / 16)) + g);
     }
   }
+  uint16_t* kr = a.k + (size_t)(t0 + i0) * a.k_tok + (size_t)h * a.k_head + 8 * sub;
+  uint16_t* vr = a.v + (size_t)(t0 + i0) * a.v_tok + (size_t)h * a.v_head + 8 * sub;
 #pragma unroll
   for (int u = 0; u < R::U; ++u) {
-    const int row = row0 + u * R::RPP + threadIdx.x / R::TPR;
     // an even group's thread loaded r = 2c of groups g, g + 1; an odd one r = 2c + 1 of g - 1, g
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? vw[u] & 0xffffu : vw[u] >> 16, 4);
-    const uint32_t v = odd ? (got | (vw[u] & 0xffff0000u)) : ((vw[u] & 0xffffu) | (got << 16));
-    if (row < rows) {
-      const int t = row / a.Hkv, h = row % a.Hkv;
-      if (place[t - t0].y >= 0) {
-        __stcs(reinterpret_cast<uint4*>(a.k + t * a.k_tok + h * a.k_head) + sub, kv4_unpack(kw[u], ks[u]));
-        __stcs(reinterpret_cast<uint4*>(a.v + t * a.v_tok + h * a.v_head) + sub, kv4_unpack(v, vs[u]));
-      }
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? vw[u] : vw[u] >> 16, 4);
+    const uint32_t v = odd ? __byte_perm(got, vw[u], 0x7610) : __byte_perm(vw[u], got, 0x5410);
+    if (any[u]) {
+      __stcs(reinterpret_cast<uint4*>(kr + u * (size_t)R::RPP * a.k_tok), kv4_unpack(kw[u], ks[u]));
+      __stcs(reinterpret_cast<uint4*>(vr + u * (size_t)R::RPP * a.v_tok), kv4_unpack(v, vs[u]));
     }
   }
 }
