@@ -130,6 +130,12 @@ nosa_status check_state(const nosa_config& c, const nosa_state* st) {
   return NOSA_OK;
 }
 
+// Bytes of the partials of `slots` slots per group.
+size_t partial_bytes(const nosa_config& c, int slots) {
+  const int G = c.Hq / c.Hkv;
+  return (size_t)n_groups(c) * slots * (kv4(c) ? kv4_part_floats(G, c.d) : G * (c.d + 2)) * 4;
+}
+
 struct WsLayout {
   size_t scores, cnt_k1, cnt_attn, copy_list, copy_count, partials, ge_mask, sel_flag, copy_cnt,
       copy_flag, units, used, att_list, e_flag, total;
@@ -149,7 +155,7 @@ WsLayout ws_layout(const nosa_config& c) {
   w.cnt_attn = off; off += up256(NG * 4);
   w.copy_list = off; off += up256(NG * (size_t)w.copy_stride * 8);
   w.copy_count = off; off += up256(NG * 4);
-  w.partials = off; off += up256(NG * part_slots(c) * (size_t)G * (c.d + 2) * 4);
+  w.partials = off; off += up256(partial_bytes(c, part_slots(c)));
   w.ge_mask = off; off += up256(NG * (size_t)words(c) * 4);
   w.sel_flag = off; off += up256(NG * kFlagStride * 4);
   w.copy_cnt = off; off += up256(NG * 4);
@@ -541,14 +547,14 @@ nosa_status dispatch_attn(const nosa_config& c, const AttnArgs& a, const CUtenso
 template <int D, int BS, bool WIDE>
 nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t s, bool finest, bool pdl) {
   using SH = AttnKv4Shape<D, BS>;
-  const size_t smem = SH::smem_bytes(x.a.G);
+  constexpr int GM = WIDE ? 8 : 4, smem = SH::template SMEM<GM>, ctas = SH::template ctas_per_sm<GM>();
   auto k = attn_kv4_kernel<D, BS, WIDE>;
   int dev = 0, sms = 0;
   NOSA_CUDA(cudaGetDevice(&dev));
   NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  x.a.W = attn_split_kv4(c.attn_split, x.a.k, x.a.total, (long long)sms * SH::ctas_per_sm(x.a.G), finest, x.pslots);
-  x.a.stages = SH::stages(x.a.G);
+  NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  x.a.W = attn_split_kv4(c.attn_split, x.a.k, x.a.total, (long long)sms * ctas, finest, x.pslots);
+  x.a.stages = SH::template stages<GM>();
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((x.a.total + x.a.W - 1) / x.a.W);
   lc.blockDim = dim3(SH::THREADS);
@@ -1118,7 +1124,7 @@ extern "C" nosa_status nosa_decode_attn_noalloc(const nosa_config* cfg, const no
              "q/sel/out NULL or misaligned");
   NOSA_CHECK(!(c.stop_tau > 0.f), "early stop visits blocks by the step's scores: use nosa_step");
   const size_t NG = n_groups(c);
-  const size_t part_bytes = up256(NG * kPartialSlots * (size_t)(c.Hq / c.Hkv) * (c.d + 2) * 4);
+  const size_t part_bytes = up256(partial_bytes(c, kPartialSlots));
   const size_t need = part_bytes + up256(NG * 4);
   if (need > kNoAllocScratchBytes)
     return fail(NOSA_ENOMEM, "nosa_decode_attn_noalloc needs %zu bytes of static scratch; the limit is %zu "

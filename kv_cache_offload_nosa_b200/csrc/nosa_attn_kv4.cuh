@@ -35,6 +35,9 @@ namespace nosa {
 constexpr int kKv4MaxStages = 16;
 constexpr int kKv4MaxSlots = 128;  // partial slots per group, at most
 
+// Floats of one partial slot: acc [G][D], then (m, l) [G], in 16-byte steps.
+__host__ __device__ constexpr int kv4_part_floats(int G, int D) { return G * D + ((2 * G + 3) & ~3); }
+
 struct AttnKv4Args {
   AttnArgs a;
   const uint8_t* k_pages;
@@ -53,25 +56,25 @@ struct AttnKv4Shape {
   static constexpr int CTAS = D == 128 ? 3 : 4;  // per SM (128 and 96 registers a thread)
   static constexpr int PAGE = kv4_page_bytes(BS, D);
   static constexpr int STAGE = 2 * PAGE;
-  // Shared memory: alignment, barriers, tasks, meeting point, q; what the merges share; the stages.
-  static size_t smem_fixed(int G) {
-    const size_t sums = (size_t)NC * D * 8 * 4, scr = (size_t)NC * G * (D + 2) * 4;
-    const size_t fac = (size_t)G * (kKv4MaxSlots + 2) * 4 + (size_t)NC * G * D * 4;
-    const size_t most = sums > scr ? (sums > fac ? sums : fac) : (scr > fac ? scr : fac);
-    return 128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * (512 + 64) + most;
-  }
-  // As many as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
-  static int stages(int G) {
-    const long long room = 227 * 1024 / CTAS - 1024 - (long long)smem_fixed(G);
-    int n = (int)(room / STAGE);
-    n = n > kKv4MaxStages ? kKv4MaxStages : n;
-    n -= n % STEP;
+  static constexpr int most(int a, int b) { return a > b ? a : b; }
+  // Shared memory for up to GM query heads a group: alignment, barriers, tasks, meeting point, q; what
+  // the sums, the warps' partials and the merge share; the stages.
+  template <int GM>
+  static constexpr int FIXED =
+      128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * (512 + 64) +
+      most(NC * D * 8 * 4, most(NC * kv4_part_floats(GM, D), GM * kKv4MaxSlots + GM + NC * GM * D) * 4);
+  // As many stages as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
+  template <int GM>
+  static constexpr int stages() {
+    const int room = (227 * 1024 / CTAS - 1024 - FIXED<GM>) / STAGE;
+    const int n = (room > kKv4MaxStages ? kKv4MaxStages : room) / STEP * STEP;
     return n < 2 ? 2 : n;
   }
-  static size_t smem_bytes(int G) { return smem_fixed(G) + (size_t)stages(G) * STAGE; }
-  static int ctas_per_sm(int G) {
-    const int fit = (int)(227 * 1024 / (smem_bytes(G) + 1024));
-    return fit < CTAS ? (fit < 1 ? 1 : fit) : CTAS;
+  template <int GM>
+  static constexpr int SMEM = FIXED<GM> + stages<GM>() * STAGE;
+  template <int GM>
+  static constexpr int ctas_per_sm() {
+    return 227 * 1024 / (SMEM<GM> + 1024) < CTAS ? 227 * 1024 / (SMEM<GM> + 1024) : CTAS;
   }
 };
 
@@ -139,23 +142,25 @@ __device__ __forceinline__ bool kv4_meeting(uint64_t* meet, uint32_t met, unsign
   return __all_sync(0xffffffffu, mbar_wait(meet, met & 1u, deadline));
 }
 
-// The last CTA of a group merges its partials p0 [nseg][G][D + 2] into outg [G][D]; two meetings.
-// Out of line: its loads in flight would cost the main loop registers.
+// The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' factors (a
+// head per warp, a segment per lane), then every NC-th segment per warp, the warps' sums last. scr:
+// shared memory for [G] x 128 factors, [G] sums and [NC][G][D] values. Two meetings. Out of line: its
+// registers would cost the main loop.
 template <int D, int NC, bool WIDE>
 __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr, int nseg, int G, uint64_t* meet,
-                               uint32_t met, unsigned long long deadline) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, GE = G * (D + 2);
-  // merge the group's partials: every segment's factor per head, then the weighted sums
-  float* fac = scr;                      // [G][nseg]
-  float* den = scr + G * kKv4MaxSlots;  // [G]
+                                       uint32_t met, unsigned long long deadline) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, GE = kv4_part_floats(G, D);
+  float* fac = scr;
+  float* den = scr + G * kKv4MaxSlots;
+  float4* add = reinterpret_cast<float4*>(den + ((G + 3) & ~3));
   for (int h = warp; h < G; h += NC) {
     float2 ml[kKv4MaxSlots / 32];
     float M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int i = 0; i < kKv4MaxSlots / 32; ++i) {
       const int sg = 32 * i + lane;
-      ml[i] = sg < nseg ? __ldcg(reinterpret_cast<const float2*>(p0 + (size_t)sg * GE + h * (D + 2)))
-                        : make_float2(-INFINITY, 0.f);
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (sg < nseg) ml[i] = __ldcg(reinterpret_cast<const float2*>(p0 + (size_t)sg * GE + G * D) + h);
       M = fmaxf(M, ml[i].x);
     }
 #pragma unroll
@@ -164,63 +169,61 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
     for (int i = 0; i < kKv4MaxSlots / 32; ++i) {
       const int sg = 32 * i + lane;
       const float f = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
-      L = fmaf(ml[i].y, f, L);
-      if (sg < nseg) fac[h * nseg + sg] = f;
+      if (sg < nseg) {
+        L = fmaf(ml[i].y, f, L);
+        fac[h * kKv4MaxSlots + sg] = f;
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) den[h] = L;
   }
-  if (!kv4_meeting(meet, met++, deadline)) return false;
-  // a warp takes every NC-th segment, a lane the same columns of all heads
-  constexpr int HG = WIDE ? 8 : 4, CP = D / 64;
-  float2 v[HG][CP];
+  if (!kv4_meeting(meet, met, deadline)) return false;
+  constexpr int E = (WIDE ? 8 : 4) * D / 128;  // four values of a head each, 32 apart
+  constexpr int AT = 8 / E;                    // segments in flight
+  const int ne = G * (D / 4);
+  float4 v[E];
 #pragma unroll
-  for (int h = 0; h < HG; ++h)
-#pragma unroll
-    for (int c = 0; c < CP; ++c) v[h][c] = make_float2(0.f, 0.f);
-  constexpr int AT = 16 / HG;  // segments in flight
+  for (int i = 0; i < E; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int sg = warp; sg < nseg; sg += AT * NC) {
-    float2 y[AT][HG][CP];
+    float4 y[AT][E];
 #pragma unroll
-    for (int i = 0; i < AT; ++i)
+    for (int t = 0; t < AT; ++t)
 #pragma unroll
-      for (int h = 0; h < HG; ++h)
+      for (int i = 0; i < E; ++i) {
+        y[t][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (sg + t * NC < nseg && lane + 32 * i < ne)
+          y[t][i] = __ldcg(reinterpret_cast<const float4*>(p0 + (size_t)(sg + t * NC) * GE) + lane + 32 * i);
+      }
 #pragma unroll
-        for (int c = 0; c < CP; ++c)
-          y[i][h][c] = (sg + i * NC < nseg && h < G)
-                           ? __ldcg(reinterpret_cast<const float2*>(p0 + (size_t)(sg + i * NC) * GE + h * (D + 2) + 2) +
-                                    lane + 32 * c)
-                           : make_float2(0.f, 0.f);
+    for (int t = 0; t < AT; ++t)
 #pragma unroll
-    for (int i = 0; i < AT; ++i)
-#pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        const float f = h < G ? fac[h * nseg + min(sg + i * NC, nseg - 1)] : 0.f;
-#pragma unroll
-        for (int c = 0; c < CP; ++c) {
-          v[h][c].x = fmaf(y[i][h][c].x, f, v[h][c].x);
-          v[h][c].y = fmaf(y[i][h][c].y, f, v[h][c].y);
-        }
+      for (int i = 0; i < E; ++i) {
+        const int h = min((lane + 32 * i) / (D / 4), G - 1);
+        const float f = fac[h * kKv4MaxSlots + min(sg + t * NC, nseg - 1)];
+        v[i].x = fmaf(y[t][i].x, f, v[i].x);
+        v[i].y = fmaf(y[t][i].y, f, v[i].y);
+        v[i].z = fmaf(y[t][i].z, f, v[i].z);
+        v[i].w = fmaf(y[t][i].w, f, v[i].w);
       }
   }
-  float2* add = reinterpret_cast<float2*>(den + G + (G & 1));  // [NC][G][D / 2]
 #pragma unroll
-  for (int h = 0; h < HG; ++h)
-#pragma unroll
-    for (int c = 0; c < CP; ++c)
-      if (h < G) add[(warp * G + h) * (D / 2) + lane + 32 * c] = v[h][c];
-  if (!kv4_meeting(meet, met++, deadline)) return false;
-  for (int e = tid; e < G * (D / 2); e += NC * 32) {
-    float2 y = add[e];
+  for (int i = 0; i < E; ++i)
+    if (lane + 32 * i < ne) add[warp * ne + lane + 32 * i] = v[i];
+  if (!kv4_meeting(meet, met + 1u, deadline)) return false;
+  for (int e = tid; e < ne; e += NC * 32) {
+    float4 y = add[e];
 #pragma unroll
     for (int w = 1; w < NC; ++w) {
-      const float2 z = add[w * G * (D / 2) + e];
+      const float4 z = add[w * ne + e];
       y.x += z.x;
       y.y += z.y;
+      y.z += z.z;
+      y.w += z.w;
     }
-    const float L = den[e / (D / 2)];
-    reinterpret_cast<float2*>(outg)[e] = L == 0.f ? make_float2(0.f, 0.f) : make_float2(y.x / L, y.y / L);
+    const float L = den[e / (D / 4)], inv = 1.f / L;
+    reinterpret_cast<float4*>(outg)[e] = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)  // no token at all
+                                                  : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
   }
   return true;
 }
@@ -235,15 +238,16 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   const int ST = a.stages;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)ST * SH::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kKv4MaxStages;
   int2* info = reinterpret_cast<int2*>(empty + kKv4MaxStages);         // a stage's block (-1: none) and length
   uint64_t* meet = reinterpret_cast<uint64_t*>(info + kKv4MaxStages);  // the consumer warps' meeting point
   int* s_flag = reinterpret_cast<int*>(meet + 1);
   uint4* sq = reinterpret_cast<uint4*>(meet + 2);              // [NG][32] a lane's q operands of a group
   float4* sz = reinterpret_cast<float4*>(sq + NG * 32);        // [NG][4] -8 sum q of columns 2 c4, 2 c4 + 1, twice
-  float* scr = reinterpret_cast<float*>(sz + NG * 4);          // [NC][G][D + 2] at a merge
+  float* scr = reinterpret_cast<float*>(sz + NG * 4);          // [NC] partials at a merge
   float4* sums = reinterpret_cast<float4*>(scr) + warp_id() * NG * 2 * 32;  // this warp's sums, between merges
+  uint8_t* stages = smem + SH::template FIXED<WIDE ? 8 : 4> - 128;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int task0 = blockIdx.x * a.W;
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
               info[sl] = make_int2(j, L);
               if (j >= 0) {
                 mbar_arrive_expect_tx(&full[sl], SH::STAGE);
-                uint8_t* st = smem + (size_t)sl * SH::STAGE;
+                uint8_t* st = stages + (size_t)sl * SH::STAGE;
                 bulk_load(st, x.k_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[sl]);
                 bulk_load(st + SH::PAGE, x.v_pages + (size_t)page * SH::PAGE, SH::PAGE, &full[sl]);
               } else {
@@ -385,6 +389,13 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   constexpr float Y0 = 65536.f + 127.f;  // what x + e is offset by below
   uint32_t met = 0u;
   auto meeting = [&]() -> bool { return kv4_meeting(meet, met++, deadline); };
+  auto clear_flags = [&](int gi) {  // every CTA of the group has passed its waits
+    if (flags) a.sel_flag[(size_t)gi * kFlagStride] = 0u;
+    if (a.e_flag) {
+      a.e_flag[(size_t)gi * kFlagStride] = 0u;
+      a.e_flag[(size_t)gi * kFlagStride + 3] = 0u;
+    }
+  };
   uint32_t kilo = 0x64006400u;  // fp16 (1024, 1024), kept in a register
   asm volatile("" : "+r"(kilo));
   int page = warp / U;  // next page of this warp, counted over the CTA's tasks
@@ -449,11 +460,10 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     for (int mt = 0; mt < 2 * NG; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
     // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0)
     float m0 = -INFINITY, m1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    bool huge = false;
     // The tensor cores truncate as they add: an error of about 2^-24 a step, all one way. Every
     // 16 units the accumulators go to sums in shared memory, held relative to (r0, r1).
     float r0 = -INFINITY, r1 = -INFINITY;
-    int since = 0;
+    int units = 0;
     auto to_sums = [&](bool first) {
       const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
 #pragma unroll
@@ -469,7 +479,6 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       r0 = m0;
       r1 = m1;
     };
-    bool kept = false;
 
     for (; page < pend; page += SH::STEP) {
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, deadline))) {
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
         return;
       }
       const int2 ti = info[s];
-      const uint8_t* st = smem + (size_t)s * SH::STAGE;
+      const uint8_t* st = stages + (size_t)s * SH::STAGE;
       const int nval = ti.x >= 0 ? ti.y - ti.x * BS - tok0 : 0;
       if (nval > 0) {
         // ---- scores of two tiles of 16 tokens: [tile][row A, row B][column]
@@ -546,12 +555,13 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
             yn1 = fmaxf(yn1, __shfl_xor_sync(0xffffffffu, yn1, o));
           }
           float mn0 = fmaxf(m0, yn0 - (Y0 + 10.f)), mn1 = fmaxf(m1, yn1 - (Y0 + 10.f));
+          // scores so large that a sum with e says little: from here on (y stays -inf) m is the
+          // largest score, found for every unit
+          const bool huge = (y0 == -INFINITY && m0 != -INFINITY) || (y1 == -INFINITY && m1 != -INFINITY) ||
+                            fabsf(yn0) > 0x1p20f || fabsf(yn1) > 0x1p20f;
           y0 = fmaxf(y0, yn0 + 3.f);
           y1 = fmaxf(y1, yn1 + 3.f);
-          huge = huge || __any_sync(0xffffffffu, fabsf(yn0) > 0x1p20f || fabsf(yn1) > 0x1p20f);
-          if (huge) {
-            // scores so large that a sum with e says little: from here on m is the largest score,
-            // found for every unit
+          if (__any_sync(0xffffffffu, huge)) {
             mn0 = fmaxf(fmaxf(xs[0][0][0], xs[0][1][0]), fmaxf(xs[1][0][0], xs[1][1][0]));
             mn1 = fmaxf(fmaxf(xs[0][0][1], xs[0][1][1]), fmaxf(xs[1][0][1], xs[1][1][1]));
 #pragma unroll
@@ -624,11 +634,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
-      if (++since == 16) {
-        to_sums(!kept);
-        kept = true;
-        since = 0;
-      }
+      if ((++units & 15) == 0) to_sums(units == 16);
       s += SH::STEP;
       if (s >= ST) {
         s -= ST;
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     }
 
     // -------------------------------------------------- this CTA's part of the group
-    if (kept) {
+    if (units >= 16) {
       const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
 #pragma unroll
       for (int mt = 0; mt < 2 * NG; ++mt) {
@@ -660,21 +666,26 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
         for (int e = 0; e < 4; ++e) acc[mt][e] += __shfl_xor_sync(0xffffffffu, acc[mt][e], 2);
     }
     ok = meeting() && ok;  // everyone has read q and its sums
+    const int GE = kv4_part_floats(a.G, D);
     if (WIDE || c4 < 2) {
       const int h0 = col_head(2 * c4), h1 = col_head(2 * c4 + 1);
       const bool cv0 = h0 < a.G, cv1 = h1 < a.G;
-      float* w0 = scr + ((size_t)warp * a.G + h0) * (D + 2);
-      float* w1 = scr + ((size_t)warp * a.G + h1) * (D + 2);
+      float* w = scr + warp * GE;
       if (r == 0) {
-        if (cv0) w0[0] = m0, w0[1] = l0;
-        if (cv1) w1[0] = m1, w1[1] = l1;
+        float2* ml = reinterpret_cast<float2*>(w + a.G * D);
+        if (cv0) ml[h0] = make_float2(m0, l0);
+        if (cv1) ml[h1] = make_float2(m1, l1);
       }
       // rows r and r + 8 of tile mt of group g: values 32g + 4r + 2mt and the next
 #pragma unroll
-      for (int mt = 0; mt < 2 * NG; ++mt) {
-        const int at = 2 + 32 * (mt / 2) + 4 * r + 2 * (mt & 1);
-        if (cv0) *reinterpret_cast<float2*>(w0 + at) = make_float2(acc[mt][0], acc[mt][2]);
-        if (cv1) *reinterpret_cast<float2*>(w1 + at) = make_float2(acc[mt][1], acc[mt][3]);
+      for (int g = 0; g < NG; ++g) {
+        const int at = 32 * g + 4 * r;
+        if (cv0)
+          *reinterpret_cast<float4*>(w + h0 * D + at) =
+              make_float4(acc[2 * g][0], acc[2 * g][2], acc[2 * g + 1][0], acc[2 * g + 1][2]);
+        if (cv1)
+          *reinterpret_cast<float4*>(w + h1 * D + at) =
+              make_float4(acc[2 * g][1], acc[2 * g][3], acc[2 * g + 1][1], acc[2 * g + 1][3]);
       }
     }
     if (!ok || !meeting()) {
@@ -682,71 +693,75 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       return;
     }
     const int first = (int)(((long long)gi * a.k) / a.W);
-    const int nseg = (int)(((long long)gi * a.k + a.k - 1) / a.W) - first + 1, seg = blockIdx.x - first;
-    const int GE = a.G * (D + 2);
-    float* outg = a.out + ((size_t)(gi / a.Hkv) * a.Hq + (gi % a.Hkv) * a.G) * D;  // [G][D]
-    {
-      // two values of a head per thread: the warps' parts, to the group's partial slot, or to the
-      // output where this CTA has the whole group
-      float* part = a.partials + ((size_t)gi * x.pslots + seg) * GE;
-      for (int e = tid; e < a.G * (D / 2); e += NC * 32) {
-        const int h = e / (D / 2), col = 2 * (e % (D / 2));
-        float M = -INFINITY, f[NC], L = 0.f;
-        float2 v = make_float2(0.f, 0.f);
+    const int nseg = (int)(((long long)gi * a.k + a.k - 1) / a.W) - first + 1;
+    // the warps' parts, four values per thread: to the output where this CTA has the whole group,
+    // else to its slot of the group's partials
+    float* part = a.partials + ((size_t)gi * x.pslots + blockIdx.x - first) * GE;
+    float* outg = a.out + ((size_t)(gi / a.Hkv) * a.Hq + (gi % a.Hkv) * a.G) * D;
+#pragma unroll 1
+    for (int e = tid; e < a.G * (D / 4); e += NC * 32) {
+      const int h = e / (D / 4);
+      float2 ml[NC];
+      float M = -INFINITY, L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NC; ++w) {
-          f[w] = scr[(w * a.G + h) * (D + 2)];
-          M = fmaxf(M, f[w]);
-        }
+      for (int w = 0; w < NC; ++w) {
+        ml[w] = reinterpret_cast<const float2*>(scr + w * GE + a.G * D)[h];
+        M = fmaxf(M, ml[w].x);
+      }
 #pragma unroll
-        for (int w = 0; w < NC; ++w) {
-          const float* ww = scr + (w * a.G + h) * (D + 2);
-          f[w] = f[w] == M ? 1.f : ex2(f[w] - M);
-          const float2 y = *reinterpret_cast<const float2*>(ww + 2 + col);
-          L = fmaf(ww[1], f[w], L);
-          v.x = fmaf(y.x, f[w], v.x);
-          v.y = fmaf(y.y, f[w], v.y);
-        }
-        if (nseg == 1) {
-          *reinterpret_cast<float2*>(outg + h * D + col) =
-              L == 0.f ? make_float2(0.f, 0.f) : make_float2(v.x / L, v.y / L);
-        } else {
-          *reinterpret_cast<float2*>(part + h * (D + 2) + 2 + col) = v;
-          if (col == 0) *reinterpret_cast<float2*>(part + h * (D + 2)) = make_float2(M, L);
-        }
+      for (int w = 0; w < NC; ++w) {
+        const float f = ml[w].x == M ? 1.f : ex2(ml[w].x - M);
+        const float4 y = reinterpret_cast<const float4*>(scr + w * GE)[e];
+        L = fmaf(ml[w].y, f, L);
+        v.x = fmaf(y.x, f, v.x);
+        v.y = fmaf(y.y, f, v.y);
+        v.z = fmaf(y.z, f, v.z);
+        v.w = fmaf(y.w, f, v.w);
+      }
+      if (nseg == 1) {
+        const float inv = 1.f / L;
+        reinterpret_cast<float4*>(outg)[e] = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)  // no token at all
+                                                      : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      } else {
+        reinterpret_cast<float4*>(part)[e] = v;
+        if (e % (D / 4) == 0) reinterpret_cast<float2*>(part + a.G * D)[h] = make_float2(M, L);
       }
     }
-    bool last = true;
-    if (nseg > 1) {
-      __threadfence();
-      ok = meeting();
-      if (ok && tid == 0) *s_flag = (atomicAdd(&a.counters[gi], 1u) == (unsigned)(nseg - 1));
-      if (!ok || !meeting()) {
+    if (nseg == 1) {
+      if (tid == 0) clear_flags(gi);
+    } else {
+      // The last CTA to publish its part (atomic ticket, no spinning) merges the group. One thread's
+      // fences stand for the CTA's: the meetings order the others before and after it.
+      if (!meeting()) {
         set_err(a.err, NOSA_ERR_TIMEOUT);
         return;
       }
-      last = *s_flag != 0;
-      if (last) {
+      if (tid == 0) {
         __threadfence();
+        *s_flag = atomicAdd(&a.counters[gi], 1u) == (unsigned)(nseg - 1);
+        __threadfence();
+      }
+      if (!meeting()) {
+        set_err(a.err, NOSA_ERR_TIMEOUT);
+        return;
+      }
+      if (*s_flag) {
         if (!kv4_merge<D, NC, WIDE>(a.partials + (size_t)gi * x.pslots * GE, outg, scr, nseg, a.G, meet, met, deadline)) {
           set_err(a.err, NOSA_ERR_TIMEOUT);
           return;
         }
         met += 2u;
-        if (tid == 0) a.counters[gi] = 0u;
+        if (tid == 0) {
+          a.counters[gi] = 0u;
+          clear_flags(gi);
+        }
       }
     }
     // the scratch turns into sums again once everyone is done with it
     if (sr < ntask && !meeting()) {
       set_err(a.err, NOSA_ERR_TIMEOUT);
       return;
-    }
-    if (last && tid == 0) {
-      if (flags) a.sel_flag[(size_t)gi * kFlagStride] = 0u;  // every CTA of the group passed its wait
-      if (a.e_flag) {
-        a.e_flag[(size_t)gi * kFlagStride] = 0u;
-        a.e_flag[(size_t)gi * kFlagStride + 3] = 0u;
-      }
     }
   }
 }
