@@ -28,35 +28,7 @@ def buffer_bytes(cfg: nosa_config) -> dict:
             "score_rows": ng * cfg.n_score_rows * cfg.d * 2,
             "block_scores": ng * cfg.max_blocks * 4, "evict": ng * cfg.max_blocks * 4,
             "sel": ng * k * 4, "miss_count": ng * 4, "used": cfg.B * cfg.Hq * 4,
-            "prefill_len": cfg.B * 4, "resident": ng * cfg.max_blocks,
-            "cu_tokens": (cfg.B + 1) * 4, "start": cfg.B * 4}
-
-
-def run_strides(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor,
-                device: torch.device) -> nosa_kv_strides:
-    """Strides of a run's K and V rows; refuses (NosaError, NOSA_EINVAL) tensors that are not
-    [n_tokens, Hkv, d] of 16-bit values on `device` with contiguous rows."""
-    want = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d)
-    strides = []
-    for name, t in (("k", k), ("v", v)):
-        if t.device != device:
-            raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
-        if t.dtype is not torch.bfloat16 and t.dtype is not torch.int16:
-            raise NosaError(NOSA_EINVAL, f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
-        if t.shape != want:
-            raise NosaError(NOSA_EINVAL, f"{name} must be {list(want)}, not {list(t.shape)}")
-        tok, head, value = t.stride()
-        if value != 1:
-            raise NosaError(NOSA_EINVAL, f"{name}'s rows must be contiguous")
-        # the stride of a dimension of size 1 says nothing
-        strides += [tok if want[0] > 1 else want[1] * want[2], head if want[1] > 1 else want[2]]
-    return nosa_kv_strides(*strides)
-
-
-def check_int32(**bufs):
-    for name, t in bufs.items():
-        if isinstance(t, torch.Tensor) and t.dtype != torch.int32:
-            raise NosaError(NOSA_EINVAL, f"{name} must be int32, not {t.dtype}")
+            "prefill_len": cfg.B * 4, "resident": ng * cfg.max_blocks}
 
 
 def check_buffer(name: str, t, nbytes: int, device: Optional[torch.device] = None):
@@ -76,6 +48,41 @@ def check_buffer(name: str, t, nbytes: int, device: Optional[torch.device] = Non
     have = t.numel() * t.element_size()
     if have < nbytes:
         raise NosaError(NOSA_EINVAL, f"{name} holds {have} bytes, the call needs {nbytes}")
+
+
+_ROW_TYPES = (torch.bfloat16, torch.int16)
+
+
+def check_run(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor, cu_tokens, start,
+              device: torch.device) -> Optional[nosa_kv_strides]:
+    """Refuses (NosaError, NOSA_EINVAL) what is not a run of tokens on `device`: k and v
+    [n_tokens, Hkv, d] of 16-bit values with contiguous rows, cu_tokens [B + 1] and start [B]
+    (or None) int32 and contiguous. Returns the rows' strides, None where both are contiguous."""
+    want, index = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d), device.index
+    for name, t in (("k", k), ("v", v)):
+        if t.get_device() != index:
+            raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
+        if t.dtype not in _ROW_TYPES:
+            raise NosaError(NOSA_EINVAL, f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
+        if t.shape != want:
+            raise NosaError(NOSA_EINVAL, f"{name} must be {list(want)}, not {list(t.shape)}")
+    for name, t, n in (("cu_tokens", cu_tokens, cfg.B + 1), ("start", start, cfg.B)):
+        if t is None and name == "start":
+            continue
+        if t.get_device() != index:
+            raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
+            raise NosaError(NOSA_EINVAL, f"{name} must be {n} contiguous int32 values, not {t.dtype} {list(t.shape)}")
+    if k.is_contiguous() and v.is_contiguous():
+        return None
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        tok, head, value = t.stride()
+        if value != 1:
+            raise NosaError(NOSA_EINVAL, f"{name}'s rows must be contiguous")
+        # the stride of a dimension of size 1 says nothing
+        strides += [tok if want[0] > 1 else want[1] * want[2], head if want[1] > 1 else want[2]]
+    return nosa_kv_strides(*strides)
 
 
 class NosaCache:
@@ -134,17 +141,13 @@ class NosaCache:
         """Quantises a run of tokens (k, v [n_tokens, Hkv, d] bf16, any strides with contiguous
         rows) into the pages of a 4-bit cache; tokens cu_tokens[b] .. cu_tokens[b+1]-1 go to
         positions start[b], ... of sequence b (start None: 0). Write the prefill, then init."""
-        self._check(cu_tokens=cu_tokens, start=start)
-        check_int32(cu_tokens=cu_tokens, start=start)
-        write_kv(self.cfg, self.state, k, v, cu_tokens, start,
-                 strides=run_strides(self.cfg, k, v, self.device), stream=stream)
+        strides = check_run(self.cfg, k, v, cu_tokens, start, self.device)
+        write_kv(self.cfg, self.state, k, v, cu_tokens, start, k.shape[0], strides, stream)
 
     def read(self, k, v, cu_tokens, start=None, stream=None):
         """Reads a run of tokens of a 4-bit cache back into k, v (as write takes them)."""
-        self._check(cu_tokens=cu_tokens, start=start)
-        check_int32(cu_tokens=cu_tokens, start=start)
-        read_kv(self.cfg, self.state, k, v, cu_tokens, start,
-                strides=run_strides(self.cfg, k, v, self.device), stream=stream)
+        strides = check_run(self.cfg, k, v, cu_tokens, start, self.device)
+        read_kv(self.cfg, self.state, k, v, cu_tokens, start, k.shape[0], strides, stream)
 
     def append(self, k_new, v_new, stream=None):
         self._check(k_new=k_new, v_new=v_new)

@@ -147,7 +147,6 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 WsLayout ws_layout(const nosa_config& c) {
   WsLayout w;
   const size_t NG = n_groups(c);
-  const int G = c.Hq / c.Hkv;
   w.copy_stride = (kk(c) + 1 > c.slots) ? kk(c) + 1 : c.slots;
   size_t off = 0;
   w.scores = off; off += up256(NG * c.max_blocks * 4);

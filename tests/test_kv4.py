@@ -11,7 +11,7 @@ import torch
 import kv4_reference as R
 import kv_cache_offload_nosa_b200 as nosa
 from kv_cache_offload_nosa_b200 import build as nb
-from kv_cache_offload_nosa_b200.cache import NosaCache, buffer_bytes, run_strides
+from kv_cache_offload_nosa_b200.cache import NosaCache, check_run
 
 
 @pytest.fixture(scope="module")
@@ -128,32 +128,43 @@ class _OnCuda(torch.Tensor):
     is_cuda = True
     device = torch.device("cuda", 0)
 
+    def get_device(self):
+        return 0
+
+
+def on_cuda(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_OnCuda)
+
 
 def test_cache_checks_the_rows_it_is_given():
-    c = cfg()
-
-    def rows(*shape, dtype=torch.bfloat16):
-        return torch.zeros(shape, dtype=dtype).as_subclass(_OnCuda)
-
-    dev = torch.device("cuda", 0)
-    s = run_strides(c, rows(5, 2, 128), rows(5, 2, 128), dev)
-    assert (s.k_tok, s.k_head, s.v_tok, s.v_head) == (256, 128, 256, 128)
-    qkv = torch.zeros(5, 12, 128, dtype=torch.bfloat16).as_subclass(_OnCuda)
-    s = run_strides(c, qkv[:, 8:10], qkv[:, 10:12], dev)
+    c, dev, rows = cfg(), torch.device("cuda", 0), on_cuda
+    cu, start = on_cuda(3, dtype=torch.int32), on_cuda(2, dtype=torch.int32)
+    assert check_run(c, rows(5, 2, 128), rows(5, 2, 128), cu, start, dev) is None
+    assert check_run(c, rows(0, 2, 128), rows(0, 2, 128), cu, None, dev) is None
+    qkv = rows(5, 12, 128)
+    s = check_run(c, qkv[:, 8:10], qkv[:, 10:12], cu, start, dev)
     assert (s.k_tok, s.k_head, s.v_tok, s.v_head) == (1536, 128, 1536, 128)
-    for k, v in [(rows(5, 2, 64), rows(5, 2, 128)), (rows(5, 2, 128), rows(4, 2, 128)),
-                 (rows(5, 2, 128, dtype=torch.float16), rows(5, 2, 128)),
-                 (rows(5, 2, 128), rows(5, 2, 128, dtype=torch.float32)), (rows(10, 128), rows(10, 128)),
-                 (rows(5, 2, 256)[..., ::2], rows(5, 2, 128)),
-                 (torch.zeros(5, 2, 128, dtype=torch.bfloat16), rows(5, 2, 128))]:
+    assert check_run(c, qkv[:1, 8:10], rows(2, 1, 128).transpose(0, 1), cu, start, dev) is None
+    s = check_run(c, qkv[:1, 8:10], rows(1, 4, 128)[:, ::2], cu, start, dev)
+    assert (s.k_tok, s.k_head, s.v_tok, s.v_head) == (256, 128, 256, 256)
+    good = rows(5, 2, 128)
+    for k, v in [(rows(5, 2, 64), good), (good, rows(4, 2, 128)), (rows(5, 2, 128, dtype=torch.float16), good),
+                 (good, rows(5, 2, 128, dtype=torch.float32)), (rows(10, 128), rows(10, 128)),
+                 (rows(5, 2, 256)[..., ::2], good), (torch.zeros(5, 2, 128, dtype=torch.bfloat16), good)]:
+        with pytest.raises(nosa.NosaError) as e:
+            check_run(c, k, v, cu, start, dev)
+        assert e.value.status == nosa.NOSA_EINVAL
+    i32 = torch.int32
+    for cu_, start_ in [(on_cuda(2, dtype=i32), start), (on_cuda(3, dtype=torch.int64), start), (cu, on_cuda(1, dtype=i32)),
+                        (cu, on_cuda(2, dtype=torch.int64)), (on_cuda(6, dtype=i32)[::2], start),
+                        (torch.zeros(3, dtype=i32), start), (cu, torch.zeros(2, dtype=i32))]:
         with pytest.raises(nosa.NosaError):
-            run_strides(c, k, v, dev)
+            check_run(c, good, good, cu_, start_, dev)
     cache = NosaCache.__new__(NosaCache)
-    cache.cfg, cache.device, cache._bytes = c, dev, buffer_bytes(c)
-    with pytest.raises(nosa.NosaError):   # a sequence's bound is missing
-        cache.write(rows(5, 2, 128), rows(5, 2, 128), torch.zeros(2, dtype=torch.int32).as_subclass(_OnCuda))
-    with pytest.raises(nosa.NosaError):   # 64-bit positions
-        cache.write(rows(5, 2, 128), rows(5, 2, 128), torch.zeros(3, dtype=torch.int64).as_subclass(_OnCuda))
+    cache.cfg, cache.device = c, dev
+    for call in (cache.write, cache.read):
+        with pytest.raises(nosa.NosaError):
+            call(good, rows(4, 2, 128), cu, start)
 
 
 def test_geometry_of_a_4_bit_cache(lib):
