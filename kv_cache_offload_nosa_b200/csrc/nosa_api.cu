@@ -419,16 +419,40 @@ int attn_split_for(int split, int k, int total, long long target, int sms, int s
   return W;
 }
 
-// The same for 4-bit pages: equal ranges, one for each CTA that the GPU holds at once, wherever
-// they cut a group. Unpacking bounds the kernel and CTAs share an SM's issue slots, so an even load
-// counts for more than whole groups (2048 blocks of 32 groups, 444 CTAs at once: 144 us with
-// W = 148, 172 us with the divisor 128; 64 blocks of 128 groups: 31 us with either 19 or 32).
-// finest: as above, up to the 16 parts that a group has there.
-int attn_split_kv4(int split, int k, int total, long long target, bool finest, int slots) {
+// The same for 4-bit pages. Unpacking bounds the kernel, and the CTAs of an SM share its issue slots,
+// so an even load counts: every CTA that the GPU holds at once gets the same number of tasks, wherever
+// that cuts a group (2048 blocks of 64 tokens, 32 groups, d = 128, 444 CTAs: 144 us in even shares of
+// 148, 149 us in ranges of 158 within the groups, 172 us in ranges of 128). But a CTA with parts of two
+// groups starts and ends a part twice, about 3 us. Ranges within the groups (parts > 0) are taken where
+// they leave no SM more than 96 Ki values of K rows over the even share, which is what it unpacks in
+// that time (64 blocks, 128 groups: 30.4 against 31.2 us; 2048 blocks, 8 groups: 47.5 against 50.4 us;
+// 77 blocks of 32 tokens, 128 groups, d = 64: 15.5 against 17.4 us).
+// finest: ranges within the groups too, up to 16 each.
+struct Kv4Split {
+  int W, parts, ctas;
+};
+
+Kv4Split attn_split_kv4(int split, int k, int total, long long target, int sms, int block_values, bool finest,
+                        int slots) {
   auto width = [&](int parts) { return (k + parts - 2) / (parts - 1); };  // a group in `parts` ranges at most
-  const int W = split > 0 ? split : finest ? width(kPartialSlots) : (int)((total + target - 1) / target);
-  const int least = width(slots);
-  return W < least ? least : (W < 1 ? 1 : W);
+  Kv4Split r;
+  r.parts = 0;
+  r.W = split > 0 ? split : (int)((total + target - 1) / target);
+  if (r.W < width(slots)) r.W = width(slots);
+  if (r.W < 1) r.W = 1;
+  if (split <= 0) {
+    const int ng = total / k;
+    long long n = finest ? kPartialSlots : target / ng;
+    n = n < 1 ? 1 : (n > slots ? slots : (n > k ? k : n));
+    const int W = (int)((k + n - 1) / n), parts = (k + W - 1) / W;
+    const long long most = ((long long)ng * parts + sms - 1) / sms * W;  // tasks of the fullest SM
+    if (finest || (most - total / sms) * block_values <= 96 * 1024) {
+      r.W = W;
+      r.parts = parts;
+    }
+  }
+  r.ctas = r.parts ? total / k * r.parts : (total + r.W - 1) / r.W;
+  return r;
 }
 
 // finest: the smallest split width the partial slots allow (used when the attention of each
@@ -552,10 +576,12 @@ nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t 
   NOSA_CUDA(cudaGetDevice(&dev));
   NOSA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   NOSA_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  x.a.W = attn_split_kv4(c.attn_split, x.a.k, x.a.total, (long long)sms * ctas, finest, x.pslots);
+  const Kv4Split sp = attn_split_kv4(c.attn_split, x.a.k, x.a.total, (long long)sms * ctas, sms, BS * D, finest, x.pslots);
+  x.a.W = sp.W;
+  x.parts = sp.parts;
   x.a.stages = SH::template stages<GM>();
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((x.a.total + x.a.W - 1) / x.a.W);
+  lc.gridDim = dim3(sp.ctas);
   lc.blockDim = dim3(SH::THREADS);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
@@ -970,8 +996,14 @@ nosa_status nosa_step_geometry(const nosa_config* cfg, int32_t host_pools, int32
   }
   // K and V pages of one block: 2 x bs x d bf16 values
   const long long at_once = (long long)sms * attn_ctas_per_sm;
-  const int W = kv4(c) ? attn_split_kv4(c.attn_split, k, total, at_once, host_pools != 0, part_slots(c))
-                       : attn_split_for(c.attn_split, k, total, at_once, sms, 4 * c.block_size * c.d, host_pools != 0);
+  if (kv4(c)) {
+    const Kv4Split sp = attn_split_kv4(c.attn_split, k, total, at_once, sms, c.block_size * c.d, host_pools != 0,
+                                       part_slots(c));
+    out->attn_tasks_per_cta = sp.W;
+    out->attn_ctas = sp.ctas;
+    return NOSA_OK;
+  }
+  const int W = attn_split_for(c.attn_split, k, total, at_once, sms, 4 * c.block_size * c.d, host_pools != 0);
   out->attn_tasks_per_cta = W;
   out->attn_ctas = (total + W - 1) / W;
   return NOSA_OK;

@@ -2,7 +2,7 @@
 //
 // The tasks, their split over CTAs and the merge of the partials are those of the bf16 kernel:
 // the B*Hkv*k (group, selected block) tasks, group after group, are cut in ranges of W, one range
-// per CTA; each range writes one partial (m, l, acc) per query head and group it touches, and the
+// per CTA (or each group in ranges of its own); each range writes one partial (m, l, acc) per query head and group it touches, and the
 // last CTA to finish a group (atomic ticket) merges them. One producer warp brings each task's K
 // and V page (two bulk copies, codes and scales together) into a ring of stages; the consumer warps
 // take 32 tokens each, a page's units going to neighbouring warps and page after page to the next.
@@ -43,6 +43,7 @@ struct AttnKv4Args {
   const uint8_t* k_pages;
   const uint8_t* v_pages;
   int pslots;  // partial slots per group
+  int parts;   // > 0: every group in this many ranges of W (the last one shorter), none across groups
 };
 
 template <int D, int BS>
@@ -250,8 +251,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   uint8_t* stages = smem + SH::template FIXED<WIDE ? 8 : 4> - 128;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int task0 = blockIdx.x * a.W;
-  const int ntask = min(a.W, a.total - task0);
+  const int task0 = x.parts ? blockIdx.x / x.parts * a.k + blockIdx.x % x.parts * a.W : blockIdx.x * a.W;
+  const int ntask = min(a.W, x.parts ? a.k - blockIdx.x % x.parts * a.W : a.total - task0);
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0)
     float m0 = -INFINITY, m1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     // The tensor cores truncate as they add: an error of about 2^-24 a step, all one way. Every
-    // 16 units the accumulators go to sums in shared memory, held relative to (r0, r1).
+    // 8 units the accumulators go to sums in shared memory, held relative to (r0, r1).
     float r0 = -INFINITY, r1 = -INFINITY;
     int units = 0;
     auto to_sums = [&](bool first) {
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
-      if ((++units & 15) == 0) to_sums(units == 16);
+      if ((++units & 7) == 0) to_sums(units == 8);
       s += SH::STEP;
       if (s >= ST) {
         s -= ST;
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     }
 
     // -------------------------------------------------- this CTA's part of the group
-    if (units >= 16) {
+    if (units >= 8) {
       const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
 #pragma unroll
       for (int mt = 0; mt < 2 * NG; ++mt) {
@@ -692,8 +693,9 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       set_err(a.err, NOSA_ERR_TIMEOUT);
       return;
     }
-    const int first = (int)(((long long)gi * a.k) / a.W);
-    const int nseg = (int)(((long long)gi * a.k + a.k - 1) / a.W) - first + 1;
+    // the group's first CTA and how many it has
+    const int first = x.parts ? gi * x.parts : gi * a.k / a.W;
+    const int nseg = x.parts ? x.parts : (gi * a.k + a.k - 1) / a.W - first + 1;
     // the warps' parts, four values per thread: to the output where this CTA has the whole group,
     // else to its slot of the group's partials
     float* part = a.partials + ((size_t)gi * x.pslots + blockIdx.x - first) * GE;

@@ -76,7 +76,7 @@ struct KvRunArgs {
 };
 
 // A CTA takes TOKENS tokens of one KV head (the heads of the same tokens are neighbouring CTAs, so
-// that a token-major row is read by CTAs that run together), a thread 8 values of K and of V.
+// that a token-major row is read by CTAs that run together); TPR threads a row for 8 values each.
 template <int D>
 struct KvRun {
   static constexpr int TPR = D / 8;            // threads per row
@@ -132,68 +132,76 @@ __device__ __forceinline__ uint32_t max_abs_bf162(uint32_t x, uint32_t y) {  // 
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// The code word of 8 values (pairs of consecutive ones) and the scale of their group, whose other
-// values the three neighbouring lanes hold. A code is the low bits of 0x4b400000 + code; the words
-// of eight add up in base 16, and their constant parts to a constant.
-__device__ __forceinline__ uint32_t kv4_pack(uint4 x, uint32_t* scale) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = max_abs_bf162(max_abs_bf162(w[0], w[1]), max_abs_bf162(w[2], w[3]));
+// The code words of 16 values (pairs of consecutive ones) and the scale of their group, whose other
+// half the neighbouring lane holds. A code is the low bits of 0x4b400000 + code; the words of eight
+// add up in base 16, and their constant parts to a constant.
+__device__ __forceinline__ uint2 kv4_pack(const uint4* x, uint32_t* scale) {
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  uint32_t m = max_abs_bf162(w[0], w[1]);
+#pragma unroll
+  for (int i = 2; i < 8; ++i) m = max_abs_bf162(m, w[i]);
   m = max_abs_bf162(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max_abs_bf162(m, __shfl_xor_sync(0xffffffffu, m, 2));
   m = max_abs_bf162(m, __byte_perm(m, m, 0x1032));
   *scale = kv4_scale(m & 0xffffu);
   const float inv = kv4_inverse(*scale);
-  uint32_t word = 0u;
+  uint32_t word[2] = {0u, 0u};
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
+  for (int i = 15; i >= 0; --i) {
     const float v = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    word = word * 16u + __float_as_uint(fmaf(v, inv, 12582912.f + 8.f));
+    word[i / 8] = word[i / 8] * 16u + __float_as_uint(fmaf(v, inv, 12582912.f + 8.f));
   }
   constexpr uint32_t BASE = 0x4b400000u * 0x11111111u;
-  return word - BASE;
+  return make_uint2(word[0] - BASE, word[1] - BASE);
 }
 
-// Writes K and V rows into their pages. Bound by issue slots before memory in its first form (83 %
-// of them at 3.2 TB/s); see KvRun for the mapping that took the index arithmetic out of the rows.
+// Writes K and V rows into their pages, 16 values of each per thread. Issue slots bound it before
+// memory does: four sequences of 32768 tokens x 8 heads (d = 128) take 198 us with eight values per
+// thread and an index division per row (83 % of the slots used), 128 us without the divisions.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_write_kernel(KvRunArgs a) {
   using R = KvRun<D>;
+  constexpr int TPR = D / 16, RPP = R::THREADS / TPR, U = R::TOKENS / RPP;
   __shared__ int2 place[R::TOKENS];
   const int h = blockIdx.x % a.Hkv, t0 = blockIdx.x / a.Hkv * R::TOKENS;
-  const int i0 = threadIdx.x / R::TPR, sub = threadIdx.x % R::TPR, g = sub >> 2, c = sub & 3;
-  uint4 kx[R::U], vx[R::U];
+  const int i0 = threadIdx.x / TPR, sub = threadIdx.x % TPR, g = sub >> 1, half = sub & 1;
+  uint4 kx[U][2], vx[U][2];
   {
-    const uint16_t* kr = a.k + (size_t)(t0 + i0) * a.k_tok + (size_t)h * a.k_head + 8 * sub;
-    const uint16_t* vr = a.v + (size_t)(t0 + i0) * a.v_tok + (size_t)h * a.v_head + 8 * sub;
+    const uint16_t* kr = a.k + (size_t)(t0 + i0) * a.k_tok + (size_t)h * a.k_head + 16 * sub;
+    const uint16_t* vr = a.v + (size_t)(t0 + i0) * a.v_tok + (size_t)h * a.v_head + 16 * sub;
 #pragma unroll
-    for (int u = 0; u < R::U; ++u) {
-      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-      if (t0 + i0 + u * R::RPP < a.n_tokens) {
-        kx[u] = __ldcs(reinterpret_cast<const uint4*>(kr + u * (size_t)R::RPP * a.k_tok));
-        vx[u] = __ldcs(reinterpret_cast<const uint4*>(vr + u * (size_t)R::RPP * a.v_tok));
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        kx[u][j] = vx[u][j] = make_uint4(0, 0, 0, 0);
+        if (t0 + i0 + u * RPP < a.n_tokens) {
+          kx[u][j] = __ldcs(reinterpret_cast<const uint4*>(kr + u * (size_t)RPP * a.k_tok) + j);
+          vx[u][j] = __ldcs(reinterpret_cast<const uint4*>(vr + u * (size_t)RPP * a.v_tok) + j);
+        }
       }
-    }
   }
   kv_run_places<D>(a, t0, h, place);
   const size_t PB = kv4_page_bytes(a.bs, D);
   const bool odd = g & 1;
 #pragma unroll
-  for (int u = 0; u < R::U; ++u) {
+  for (int u = 0; u < U; ++u) {
     uint32_t ks, vs;
-    const uint32_t kw = kv4_pack(kx[u], &ks), w = kv4_pack(vx[u], &vs);
-    // V: this thread's values are the words of r = 2c (low half) and r = 2c + 1 of group g; the
-    // thread of the other group of a pair takes one of them, so that each stores 4 bytes
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, 4);
-    const uint32_t vw = odd ? __byte_perm(got, w, 0x7610) : __byte_perm(w, got, 0x5410);
-    const int2 at = place[i0 + u * R::RPP];
+    const uint2 kw = kv4_pack(kx[u], &ks), w = kv4_pack(vx[u], &vs);
+    // V: a thread's words hold r = 4 half + 0, 1 and + 2, 3 of group g. The thread of the other group
+    // of a pair takes one of the words and gives its other, so that each stores two times 4 bytes.
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w.x : w.y, 2);
+    const uint32_t lo = odd ? got : w.x, hi = odd ? w.y : got;  // even group, odd group
+    const int2 at = place[i0 + u * RPP];
     if (at.x >= 0) {
       uint8_t* kp = a.k_pages + at.x * PB;
       uint8_t* vp = a.v_pages + at.x * PB;
-      *reinterpret_cast<uint32_t*>(kp + at.y * (D / 2) + c * (D / 8) + 4 * g) = kw;
-      *reinterpret_cast<uint32_t*>(vp + at.y * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)) = vw;
-      if (c < 2)
-        *(reinterpret_cast<uint16_t*>((c ? vp : kp) + a.bs * (D / 2) + at.y * (D / 16)) + g) =
-            static_cast<uint16_t>(c ? vs : ks);
+      uint8_t* kc = kp + at.y * (D / 2) + 2 * half * (D / 8) + 4 * g;
+      uint8_t* vc = vp + at.y * (D / 2) + (4 * half + 2 * odd) * (D / 16) + 4 * (g >> 1);
+      *reinterpret_cast<uint32_t*>(kc) = kw.x;
+      *reinterpret_cast<uint32_t*>(kc + D / 8) = kw.y;
+      *reinterpret_cast<uint32_t*>(vc) = __byte_perm(lo, hi, 0x5410);
+      *reinterpret_cast<uint32_t*>(vc + D / 16) = __byte_perm(lo, hi, 0x7632);
+      *(reinterpret_cast<uint16_t*>((half ? vp : kp) + a.bs * (D / 2) + at.y * (D / 16)) + g) =
+          static_cast<uint16_t>(half ? vs : ks);
     }
   }
 }
@@ -217,7 +225,7 @@ __device__ __forceinline__ uint4 kv4_unpack(uint32_t w, uint32_t scale) {
 
 // Reads rows back as bf16: the write's layout of threads the other way round.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(KvRunArgs a) {
+__global__ void __launch_bounds__(256, 5) kv4_read_kernel(KvRunArgs a) {
   using R = KvRun<D>;
   __shared__ int2 place[R::TOKENS];
   const int h = blockIdx.x % a.Hkv, t0 = blockIdx.x / a.Hkv * R::TOKENS;

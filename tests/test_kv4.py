@@ -168,10 +168,29 @@ def test_cache_checks_the_rows_it_is_given():
 
 
 def test_geometry_of_a_4_bit_cache(lib):
-    """Every group's segments fit its partial slots, and every task is covered."""
-    for B, k, nbk in ((1, 1, 1), (1, 16, 64), (16, 64, 514), (1, 2048, 2048), (64, 32, 257), (3, 8192, 8192)):
-        c = cfg(B=B, Hq=8, Hkv=2, k_q=k, k_e=0, max_blocks=nbk)
+    """The tasks are covered, and no group has more ranges than partial slots."""
+    for B, k, nbk in ((1, 1, 1), (1, 16, 64), (16, 64, 514), (1, 2048, 2048), (64, 32, 257), (3, 8192, 8192), (5000, 3, 3)):
         for host in (False, True):
-            g = nosa.step_geometry(c, host, 148, 4)
-            W = g["attn_tasks_per_cta"]
-            assert 1 <= W and g["attn_ctas"] == -(-B * 2 * k // W)
+            for split in (0, 1, 5, 100):
+                g = nosa.step_geometry(cfg(B=B, k_q=k, k_e=0, max_blocks=nbk, attn_split=split), host, 148, 3)
+                W, ctas, ng = g["attn_tasks_per_cta"], g["attn_ctas"], 2 * B
+                slots = min(max(16, -(-1184 // ng)), 128)
+                linear, aligned = -(-ng * k // W), ng * -(-k // W)
+                assert ctas in (linear, aligned)
+                if ctas == aligned:
+                    assert -(-k // W) <= slots
+                else:
+                    assert -(-(k - 1) // W) + 1 <= slots
+                if split:
+                    assert W >= split and ctas == linear
+
+
+def test_split_of_a_4_bit_cache(lib):
+    """Even shares over long axes; ranges within the groups where that costs the fullest SM little."""
+    def g(**kw):
+        x = nosa.step_geometry(cfg(**kw), False, 148, 4 if kw.get("d") == 64 else 3)
+        return x["attn_tasks_per_cta"], x["attn_ctas"]
+
+    assert g(B=4, Hq=32, Hkv=8, k_q=2048, k_e=0, max_blocks=2048) == (148, 443)
+    assert g(B=8, Hq=16, Hkv=16, d=64, block_size=32, k_q=77, k_e=0, max_blocks=256) == (20, 512)
+    assert g(B=1, Hq=8, Hkv=2, d=64, k_q=16, k_e=0, max_blocks=65) == (1, 32)
