@@ -22,7 +22,8 @@
 // range for every scale of V: the reference m is 10 below the largest x_t + e_t seen, where e_t is
 // about the base-2 logarithm of the token's largest V scale, and it moves only when an x_t + e_t
 // exceeds it by more than 13. Weights are thus below 2^15, and one of 2^-14 of the largest still
-// has all 22 bits of its two parts.
+// has all 22 bits of its two parts. (e_t is at least -90, which keeps p and its sum finite: V below
+// 2^-100 loses digits, and below 2^-120 vanishes. Above 2^112 weights under 2^-11 of the largest do.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -536,13 +537,13 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
         }
         // The bf16 bits of a scale, as an integer over 128, are its base-2 logarithm plus 127 within
         // 0.09. 0x4b000000 + bits is 2^23 + bits as a float: over 128 that is Y0 + e. (e is at least
-        // -60, so that 2^-e and sums of it stay finite.)
+        // -90, so that 2^-e and sums of it stay finite.)
         float yn0 = -INFINITY, yn1 = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            float top = 0x1p-60f;
+            float top = 0x1p-90f;
 #pragma unroll
             for (int g = 0; g < NG / 2; ++g) top = fmaxf(top, fmaxf(bf16_lo(sv[t][b][g]), bf16_hi(sv[t][b][g])));
             const float e = 0x1p-7f * __uint_as_float(__byte_perm(__float_as_uint(top), 0x4b000000u, 0x7632));
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
           }
           float mn0 = fmaxf(m0, yn0 - (Y0 + 10.f)), mn1 = fmaxf(m1, yn1 - (Y0 + 10.f));
           // scores so large that a sum with e says little: from here on (y stays -inf) m is the
-          // largest score, found for every unit
+          // largest score, found for every unit, and subtracted here
           const bool huge = (y0 == -INFINITY && m0 != -INFINITY) || (y1 == -INFINITY && m1 != -INFINITY) ||
                             fabsf(yn0) > 0x1p20f || fabsf(yn1) > 0x1p20f;
           y0 = fmaxf(y0, yn0 + 3.f);
@@ -570,8 +571,17 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
               mn0 = fmaxf(mn0, __shfl_xor_sync(0xffffffffu, mn0, o));
               mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
             }
-            mn0 = fmaxf(m0, mn0 * f0);
-            mn1 = fmaxf(m1, mn1 * f1);
+            mn0 = fmaxf(m0, __fmul_rn(mn0, f0));
+            mn1 = fmaxf(m1, __fmul_rn(mn1, f1));
+            // x - m with x rounded as m was (the fused form below would keep what m lost)
+            const float z0 = mn0 == -INFINITY ? 0.f : mn0, z1 = mn1 == -INFINITY ? 0.f : mn1;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                xs[t][b][0] = (__fmul_rn(xs[t][b][0], f0) - z0) / f0;
+                xs[t][b][1] = (__fmul_rn(xs[t][b][1], f1) - z1) / f1;
+              }
             y0 = y1 = -INFINITY;
           }
           const float al0 = mn0 == m0 ? 1.f : ex2(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2(m1 - mn1);
@@ -587,7 +597,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
             acc[mt][3] *= al1;
           }
         }
-        const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
+        // (y at -inf: nothing seen, or m has been subtracted above)
+        const float mu0 = y0 == -INFINITY ? 0.f : m0, mu1 = y1 == -INFINITY ? 0.f : m1;
         // ---- O^T += (c - 8)^T . (p s)^T
 #pragma unroll
         for (int t = 0; t < 2; ++t) {

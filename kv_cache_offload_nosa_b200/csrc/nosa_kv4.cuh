@@ -114,7 +114,7 @@ __device__ __forceinline__ void kv_run_places(const KvRunArgs& a, int t0, int h,
     int2 at = make_int2(-1, 0);
     const int c0 = small ? cu_s[lo] : a.cu_tokens[lo], c1 = small ? cu_s[lo + 1] : a.cu_tokens[lo + 1];
     if (t >= c0 && t < c1 && t < a.n_tokens) {
-      const long long p = (long long)(small ? start_s[lo] : a.start ? a.start[lo] : 0) + (t - c0);
+      const long long p = (long long)(small ? start_s[lo] : a.start ? a.start[lo] : 0) + t - c0;
       if (p >= 0 && p < a.max_tokens)
         at = make_int2((lo * a.Hkv + h) * a.pages_per_group + (static_cast<int>(p) >> shift),
                        static_cast<int>(p) & (a.bs - 1));
@@ -156,7 +156,8 @@ __device__ __forceinline__ uint2 kv4_pack(const uint4* x, uint32_t* scale) {
 
 // Writes K and V rows into their pages, 16 values of each per thread. Issue slots bound it before
 // memory does: four sequences of 32768 tokens x 8 heads (d = 128) take 198 us with eight values per
-// thread and an index division per row (83 % of the slots used), 128 us without the divisions.
+// thread and index divisions per row (83 % of the slots used), 128 us without the divisions, 106 us
+// with 16 values, so that the scale is found by two threads instead of four (6.5 TB/s).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_write_kernel(KvRunArgs a) {
   using R = KvRun<D>;
@@ -223,9 +224,11 @@ __device__ __forceinline__ uint4 kv4_unpack(uint32_t w, uint32_t scale) {
                     __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
 }
 
-// Reads rows back as bf16: the write's layout of threads the other way round.
+// Reads rows back as bf16, 8 values of K and of V per thread. Bound by memory once enough CTAs are
+// resident to cover the two round trips (places, codes) before the stores: the sequences above take
+// 114 us with 48 registers (five CTAs an SM), 111 us with 40 (six), 119 us with 32 (eight).
 template <int D>
-__global__ void __launch_bounds__(256, 5) kv4_read_kernel(KvRunArgs a) {
+__global__ void __launch_bounds__(256, 6) kv4_read_kernel(KvRunArgs a) {
   using R = KvRun<D>;
   __shared__ int2 place[R::TOKENS];
   const int h = blockIdx.x % a.Hkv, t0 = blockIdx.x / a.Hkv * R::TOKENS;

@@ -159,6 +159,27 @@ def test_write_in_chunks_equals_one_write():
         assert torch.equal(a, b)
 
 
+def test_many_sequences():
+    """More sequences than the kernels keep the bounds of at hand, some of them empty."""
+    rng = np.random.default_rng(12)
+    B = 300
+    lens = rng.integers(0, 4, B)
+    start = rng.integers(0, 29, B)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    k, v = bf16_rows(rng, cu[-1], 1, 64), bf16_rows(rng, cu[-1], 1, 64)
+    cache = make_cache(B, 1, 1, 64, 32, 1, 1)
+    for p in pools(cache):
+        p.fill_(0xA5)
+    cut, st = dev(cu.astype(np.int32)), dev(start.astype(np.int32))
+    cache.write(dev(k), dev(v), cut, st)
+    check_pages(cache, expected_pages(cache, k, v, cu, start, 0xA5))
+    ko, vo = (torch.empty(int(cu[-1]), 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache.read(ko, vo, cut, st)
+    for got, bits in ((ko, k), (vo, v)):
+        ref = R.round_to_bf16(R.dequantise(*R.quantise(bits)))
+        assert np.array_equal(R.values(got.view(torch.int16).cpu().numpy().view(np.uint16)), R.values(ref))
+
+
 def test_rows_of_no_sequence_and_positions_outside_are_skipped():
     rng = np.random.default_rng(10)
     k, v = bf16_rows(rng, 40, 2, 64), bf16_rows(rng, 40, 2, 64)
@@ -289,7 +310,7 @@ ATTEND = [  # d, bs, G, Hkv, lengths, k
 
 
 @pytest.mark.parametrize("d,bs,G,Hkv,lens,k", ATTEND)
-@pytest.mark.parametrize("split", [0, 3])
+@pytest.mark.parametrize("split", [0, 3, 150])
 def test_attention(d, bs, G, Hkv, lens, k, split):
     rng = np.random.default_rng(1000 + d + bs + G + k)
     nb = max(-(-max(lens) // bs), k)
@@ -316,6 +337,56 @@ def test_attention_over_wide_ranges(qs, ks, vs):
     out = torch.empty(8 * 128, device="cuda")
     cache.decode_attn(dev(q), dev(sel), out)
     check_attention(cache, q, sel, out, K, V)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_beyond_any_softmax(sign):
+    """Scores of 10^8 and more: the largest takes all the weight (here it leads by far more than an fp32
+    score can be off by), whatever came before it, and large negative ones alone are no different."""
+    rng = np.random.default_rng(83)
+    cache = make_cache(1, 4, 1, 128, 64, 6, 6)
+    n = 380
+    k = R.syn.round_bf16(rng.standard_normal((n, 1, 128)) * 1e4).reshape(n, 1, 128)
+    v = bf16_rows(rng, n, 1, 128)
+    q = R.syn.round_bf16(rng.standard_normal((1, 4, 128)) * 1e5).reshape(1, 4, 128)
+    if sign < 0:      # every score negative: keys against the mean query
+        q = np.repeat(q[:, :1], 4, 1)
+        k = R.syn.round_bf16(-R.values(q[0, 0]) * rng.uniform(0.1, 0.3, (n, 1, 1))).reshape(n, 1, 128)
+    cache.write(dev(k), dev(v), dev(np.array([0, n], np.int32)))
+    cache.init(dev(np.array([n], np.int32)))
+    K, V = R.dequantise(*R.quantise(k))[:, 0], R.dequantise(*R.quantise(v))[:, 0]
+    out = torch.empty(4, 128, device="cuda")
+    cache.decode_attn(dev(q), dev(np.arange(6, dtype=np.int32)[None]), out)
+    x = R.values(q)[0] @ K.T * 128**-0.5
+    off = 132 * 2.0**-23 * 128**-0.5 * (np.abs(R.values(q)[0]) @ np.abs(K).T).max()
+    got = out.cpu().numpy()
+    assert np.abs(x).max() > 1e6 and np.isfinite(got).all()
+    for h in range(4):
+        top = np.argsort(x[h])[::-1]
+        lead = x[h][top[0]] - x[h][top[1]]
+        if lead > 2 * off + 100:
+            # one weight of 1: its hi + lo parts and the two divisions, 2^-21 each at most
+            assert np.abs(got[h] - V[top[0]]).max() <= 2.0**-20 * np.abs(V[top[0]]).max()
+        else:
+            close = x[h] > x[h][top[0]] - 2 * off - 100     # a mean of these rows
+            lo, hi = V[close].min(0), V[close].max(0)
+            assert ((got[h] >= lo - 1e-5) & (got[h] <= hi + 1e-5)).all()
+
+
+@pytest.mark.parametrize("vs", [1e30, 1e36, 1e-27, 1e-34])
+def test_values_at_the_ends_of_the_range(vs):
+    rng = np.random.default_rng(84)
+    cache = make_cache(1, 8, 1, 64, 32, 5, 5)
+    K, V = fill(cache, rng, [150], 1.0, vs)
+    q = bf16_rows(rng, 1, 8, 64)
+    out = torch.empty(8, 64, device="cuda")
+    cache.decode_attn(dev(q), dev(np.arange(5, dtype=np.int32)[None]), out)
+    want = R.attend(R.values(q)[0], K[0], V[0], float(np.float32(cache.cfg.scale)))
+    # V of 1e-34 has scales of about 2^-115, so the weights are about 2^(100 - 115) and their two fp16
+    # parts hold 2^-25: 2^-10 of them. V of 1e36 (2^119, scales 2^117) drops weights below
+    # 2^(-126 + 107) of the largest: 150 of 2^-19. Otherwise the ordinary bound, 1e-5 here.
+    tol = 2.0**-9 if vs == 1e-34 else 150 * 2.0**-18 if vs == 1e36 else 1e-5
+    assert np.abs(out.cpu().numpy() - want).max() <= tol * np.abs(want).max()
 
 
 def test_attention_with_unlike_scales_in_a_sequence():
