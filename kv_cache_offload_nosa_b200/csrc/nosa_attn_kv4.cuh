@@ -11,13 +11,11 @@
 //   score:  sum_d q_d K_td = sum_g s_tg sum_{d in g} q_d (c_td - 8),
 //   output: sum_t p_t V_td = sum_t (p_t s_tg) (c_td - 8),
 // so the matrix products run on the codes, and the scales enter where there are few values: the
-// per-group partial scores, and the weights. Codes become fp16 operands in registers:
-//   K: (w & 0x000f000f) is a pair of fp16 subnormals c 2^-24, (w & 0x00f000f0) is 16 c 2^-24; q is
-//      scaled by a power of two to an fp16 row (its 16ths for the second kind), and the
-//      accumulators start at -8 sum q. One mask and no arithmetic per pair.
-//   V: the same masks or'ed with 1024 (0x6400) give 1024 + c and 1024 + 16 c, and one fp16 FMA
-//      makes c - 8 of either: over a long axis the offset has to go before the sum, which it would
-//      exceed many times.
+// per-group partial scores, and the weights. Codes become fp16 operands in registers: a word's pairs
+// of codes 16 bits apart, masked and or'ed with 1024, are the fp16 pair 1024 + c, or 1024 + 16 c of the
+// next code, and one fp16 FMA makes c - 8 of either. (The offset has to go before the products: as a
+// start value -8 sum q of the accumulators it cost the scores a bit and a half, 8e-7 against 3e-7 of
+// the output, for 2 % of the time.) q is scaled by a power of two to an fp16 row.
 // The weights p_t s_tg, p_t = 2^(x_t - m), are split in two fp16 parts. They are kept in fp16's
 // range for every scale of V: the reference m is 10 below the largest x_t + e_t seen, where e_t is
 // about the base-2 logarithm of the token's largest V scale, and it moves only when an x_t + e_t
@@ -63,7 +61,7 @@ struct AttnKv4Shape {
   // the sums, the warps' partials and the merge share; the stages.
   template <int GM>
   static constexpr int FIXED =
-      128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * (512 + 64) +
+      128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * 512 +
       most(NC * D * 8 * 4, most(NC * kv4_part_floats(GM, D), GM * kKv4MaxSlots + GM + NC * GM * D) * 4);
   // As many stages as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
   template <int GM>
@@ -119,6 +117,14 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(m), "r"(o));
   return y;
+}
+// c - 8 of the codes in bits 0..3, or 4..7, of both halves of w as fp16 pairs; kilo: (1024, 1024), in
+// a register so that masking and or'ing are one instruction.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t kilo) {
+  return hfma2_u32(and_or(w, 0x000f000fu, kilo), 0x3c003c00u, 0xe408e408u);  // 1, -1032
+}
+__device__ __forceinline__ uint32_t next_code_pair(uint32_t w, uint32_t kilo) {
+  return hfma2_u32(and_or(w, 0x00f000f0u, kilo), 0x2c002c00u, 0xd480d480u);  // 1/16, -72
 }
 __device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
 template <int N>
@@ -246,8 +252,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   uint64_t* meet = reinterpret_cast<uint64_t*>(info + kKv4MaxStages);  // the consumer warps' meeting point
   int* s_flag = reinterpret_cast<int*>(meet + 1);
   uint4* sq = reinterpret_cast<uint4*>(meet + 2);              // [NG][32] a lane's q operands of a group
-  float4* sz = reinterpret_cast<float4*>(sq + NG * 32);        // [NG][4] -8 sum q of columns 2 c4, 2 c4 + 1, twice
-  float* scr = reinterpret_cast<float*>(sz + NG * 4);          // [NC] partials at a merge
+  float* scr = reinterpret_cast<float*>(sq + NG * 32);          // [NC] partials at a merge
   float4* sums = reinterpret_cast<float4*>(scr) + warp_id() * NG * 2 * 32;  // this warp's sums, between merges
   uint8_t* stages = smem + SH::template FIXED<WIDE ? 8 : 4> - 128;
 
@@ -426,34 +431,23 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 13 - exponent, kept where both it and what undoes it are floats
+      // 2^e takes the largest there; e is kept where 2^e and 2^-e are floats
       const int e = min(max(140 - static_cast<int>(mx >> 7), -100), 100);
-      const float up = __uint_as_float((127 + e) << 23), up16 = up * 0.0625f;
-      const float fq = __uint_as_float((127 - e) << 23) * a.scale_log2 * 0x1p24f;
+      const float up = __uint_as_float((127 + e) << 23);
+      const float fq = __uint_as_float((127 - e) << 23) * a.scale_log2;
       // from column r of B (all four c4 lanes agree) to columns 2 c4, 2 c4 + 1 of C
       f0 = __shfl_sync(0xffffffffu, fq, 8 * c4);
       f1 = __shfl_sync(0xffffffffu, fq, 8 * c4 + 4);
-      // warp g leaves group g's operands in shared memory (all of them would take 24 registers)
+      // warp g leaves group g's operands in shared memory (all of them would take 16 registers)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         if (g != warp) continue;
         const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};  // values (0, 1) .. (6, 7)
-        // even codes take q, odd ones a 16th of it; the fragments pair codes i and i + 4
-        const uint32_t qb[4] = {pack_f16(bf16_lo(w[0]) * up, bf16_lo(w[2]) * up),
-                                pack_f16(bf16_hi(w[0]) * up16, bf16_hi(w[2]) * up16),
-                                pack_f16(bf16_lo(w[1]) * up, bf16_lo(w[3]) * up),
-                                pack_f16(bf16_hi(w[1]) * up16, bf16_hi(w[3]) * up16)};
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 q2 = __half22float2(*reinterpret_cast<const __half2*>(&qb[j]));
-          z += ((j & 1) ? 16.f : 1.f) * (q2.x + q2.y);
-        }
-        z += __shfl_xor_sync(0xffffffffu, z, 1);
-        z += __shfl_xor_sync(0xffffffffu, z, 2);
-        z *= -8.f * 0x1p-24f;
-        sq[g * 32 + lane] = make_uint4(qb[0], qb[1], qb[2], qb[3]);
-        if (c4 < 2) reinterpret_cast<float*>(sz + g * 4 + (r >> 1))[2 * c4 + (r & 1)] = z;
+        // the fragments pair codes i and i + 4
+        sq[g * 32 + lane] = make_uint4(pack_f16(bf16_lo(w[0]) * up, bf16_lo(w[2]) * up),
+                                       pack_f16(bf16_hi(w[0]) * up, bf16_hi(w[2]) * up),
+                                       pack_f16(bf16_lo(w[1]) * up, bf16_lo(w[3]) * up),
+                                       pack_f16(bf16_hi(w[1]) * up, bf16_hi(w[3]) * up));
       }
     }
     bool ok = meeting();
@@ -463,7 +457,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0)
     float m0 = -INFINITY, m1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     // The tensor cores truncate as they add: an error of about 2^-24 a step, all one way. Every
-    // 8 units the accumulators go to sums in shared memory, held relative to (r0, r1).
+    // 16 units the accumulators go to sums in shared memory, held relative to (r0, r1).
     float r0 = -INFINITY, r1 = -INFINITY;
     int units = 0;
     auto to_sums = [&](bool first) {
@@ -508,13 +502,12 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const uint4 qb = sq[g * 32 + lane];
-            const float4 qz = sz[g * 4 + c4];
+            const uint32_t kh = ka[g] >> 8, lh = kb[g] >> 8;
             float c[4];
-            mma_f16(c, ka[g] & 0x000f000fu, kb[g] & 0x000f000fu, ka[g] & 0x00f000f0u, kb[g] & 0x00f000f0u, qb.x, qb.y,
-                    qz.x, qz.y, qz.z, qz.w);
-            const uint32_t ah = ka[g] >> 8, bh = kb[g] >> 8;
-            mma_f16(c, ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u, bh & 0x00f000f0u, qb.z, qb.w, c[0], c[1],
-                    c[2], c[3]);
+            mma_f16(c, code_pair(ka[g], kilo), code_pair(kb[g], kilo), next_code_pair(ka[g], kilo),
+                    next_code_pair(kb[g], kilo), qb.x, qb.y, 0.f, 0.f, 0.f, 0.f);
+            mma_f16(c, code_pair(kh, kilo), code_pair(lh, kilo), next_code_pair(kh, kilo), next_code_pair(lh, kilo),
+                    qb.z, qb.w, c[0], c[1], c[2], c[3]);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const float sc = (g & 1) ? bf16_hi(sk[b][g / 2]) : bf16_lo(sk[b][g / 2]);
@@ -632,11 +625,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
               const uint32_t sel = 0x4400u + 0x1111u * (2 * (g & 1) + mt);  // byte 2 (g & 1) + mt of both tokens
               const uint32_t u = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
               const uint32_t v = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-              constexpr uint32_t ONE = 0x3c003c00u, M1032 = 0xe408e408u, SIXTEENTH = 0x2c002c00u, M72 = 0xd480d480u;
-              const uint32_t a0 = hfma2_u32(and_or(u, 0x000f000fu, kilo), ONE, M1032);
-              const uint32_t a1 = hfma2_u32(and_or(u, 0x00f000f0u, kilo), SIXTEENTH, M72);
-              const uint32_t a2 = hfma2_u32(and_or(v, 0x000f000fu, kilo), ONE, M1032);
-              const uint32_t a3 = hfma2_u32(and_or(v, 0x00f000f0u, kilo), SIXTEENTH, M72);
+              const uint32_t a0 = code_pair(u, kilo), a1 = next_code_pair(u, kilo);
+              const uint32_t a2 = code_pair(v, kilo), a3 = next_code_pair(v, kilo);
               float* o = acc[2 * g + mt];
               mma_f16(o, a0, a1, a2, a3, b0, b1, o[0], o[1], o[2], o[3]);
               if constexpr (WIDE) mma_f16(o, a0, a1, a2, a3, d0, d1, o[0], o[1], o[2], o[3]);
@@ -646,7 +636,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
-      if ((++units & 7) == 0) to_sums(units == 8);
+      if ((++units & 15) == 0) to_sums(units == 16);
       s += SH::STEP;
       if (s >= ST) {
         s -= ST;
@@ -655,7 +645,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     }
 
     // -------------------------------------------------- this CTA's part of the group
-    if (units >= 8) {
+    if (units >= 16) {
       const float al0 = r0 == m0 ? 1.f : ex2(r0 - m0), al1 = r1 == m1 ? 1.f : ex2(r1 - m1);
 #pragma unroll
       for (int mt = 0; mt < 2 * NG; ++mt) {
