@@ -425,8 +425,9 @@ int attn_split_for(int split, int k, int total, long long target, int sms, int s
 // 148, 149 us in ranges of 158 within the groups, 172 us in ranges of 128). But a CTA with parts of two
 // groups starts and ends a part twice, about 3 us. Ranges within the groups (parts > 0) are taken where
 // they leave no SM more than 96 Ki values of K rows over the even share, which is what it unpacks in
-// that time (64 blocks, 128 groups: 30.4 against 31.2 us; 2048 blocks, 8 groups: 47.5 against 50.4 us;
-// 77 blocks of 32 tokens, 128 groups, d = 64: 15.5 against 17.4 us).
+// that time (64 blocks, 128 groups: 30.4 against 31.2 us; 2048 blocks, 8 groups: 47.6 against 50.4 us;
+// 77 blocks of 32 tokens, 128 groups, d = 64: 15.1 against 17.4 us). With fewer than about two CTAs an
+// SM nothing covers their latencies (the last case with one range a group: 18.5 us).
 // finest: ranges within the groups too, up to 16 each.
 struct Kv4Split {
   int W, parts, ctas;
@@ -441,12 +442,23 @@ Kv4Split attn_split_kv4(int split, int k, int total, long long target, int sms, 
   if (r.W < width(slots)) r.W = width(slots);
   if (r.W < 1) r.W = 1;
   if (split <= 0) {
+    // ranges a group: what leaves the fullest SM the fewest tasks, while there are two CTAs an SM
     const int ng = total / k;
     long long n = finest ? kPartialSlots : target / ng;
     n = n < 1 ? 1 : (n > slots ? slots : (n > k ? k : n));
-    const int W = (int)((k + n - 1) / n), parts = (k + W - 1) / W;
-    const long long most = ((long long)ng * parts + sms - 1) / sms * W;  // tasks of the fullest SM
-    if (finest || (most - total / sms) * block_values <= 96 * 1024) {
+    long long least = 0;
+    int W = 0, parts = 0;
+    for (; n >= 1; --n) {
+      const int w = (int)((k + n - 1) / n), p = (k + w - 1) / w;
+      const long long most = ((long long)ng * p + sms - 1) / sms * w;
+      if (W && (finest || (long long)ng * p * 20 < 38LL * sms)) break;
+      if (!W || most < least) {
+        least = most;
+        W = w;
+        parts = p;
+      }
+    }
+    if (finest || (least - total / sms) * block_values <= 96 * 1024) {
       r.W = W;
       r.parts = parts;
     }

@@ -192,5 +192,6 @@ def test_split_of_a_4_bit_cache(lib):
         return x["attn_tasks_per_cta"], x["attn_ctas"]
 
     assert g(B=4, Hq=32, Hkv=8, k_q=2048, k_e=0, max_blocks=2048) == (148, 443)
-    assert g(B=8, Hq=16, Hkv=16, d=64, block_size=32, k_q=77, k_e=0, max_blocks=256) == (20, 512)
+    assert g(B=8, Hq=16, Hkv=16, d=64, block_size=32, k_q=77, k_e=0, max_blocks=256) == (26, 384)
+    assert g(B=6, Hq=64, Hkv=8, block_size=128, k_q=24, k_e=0, max_blocks=128) == (4, 288)
     assert g(B=1, Hq=8, Hkv=2, d=64, k_q=16, k_e=0, max_blocks=65) == (1, 32)
