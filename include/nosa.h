@@ -188,7 +188,8 @@ nosa_status nosa_state_init(const nosa_config* cfg, const nosa_state* st, const 
  * nosa_write_kv quantises the rows into the pages: the device pools, or with host pools the host
  * copy (over UVA). It changes nothing else: write the prefill, then call nosa_state_init, which
  * clears the error word (call nosa_check_device before it to see a write's fault). Reading is the
- * same call with k and v as outputs, from the same pools; rows must not overlap. n_tokens * Hkv
+ * same call with k and v as outputs, rounded to nearest even (a value within 2^-8 of the largest
+ * bf16 may come back as infinity), from the same pools; rows must not overlap. n_tokens * Hkv
  * < 2^30.
  */
 typedef struct nosa_kv_strides {
@@ -284,7 +285,7 @@ nosa_status nosa_step_launches(const nosa_config* cfg, const nosa_state* st, int
 /*
  * Launch geometry of the step's kernels for this configuration on a GPU with `sms` SMs on which
  * `attn_ctas_per_sm` attention CTAs are resident at once (two on a B200 with 64-token blocks and
- * d = 128), as nosa_step (given no events) chooses it:
+ * d = 128, bf16 pages), as nosa_step (given no events) chooses it:
  *   score_chunk        sub-blocks per score CTA: the fewest equal chunks of at most 384 that
  *                      cover the group's sub-blocks, rounded up to 64, and for small batches at
  *                      least about three score CTAs per SM in all (chunks down to 64);
@@ -296,6 +297,9 @@ nosa_status nosa_step_launches(const nosa_config* cfg, const nosa_state* st, int
  *                      between a quarter of the SMs and one wave; with early stop one CTA per
  *                      group;
  *   attn_ctas          attention CTAs.
+ * With kv_bits = 4 (three CTAs per SM at d = 128, four at d = 64) the attention's tasks are cut in even
+ * shares, one per resident CTA, or each group in ranges of its own where the fullest SM then gets
+ * little more than an even share; attn_tasks_per_cta is the longest range.
  * host_pools: nonzero for a state with host pools. No CUDA call. Errors: NOSA_EINVAL for a bad
  * configuration, sms or attn_ctas_per_sm < 1, or a NULL out.
  */
@@ -352,7 +356,8 @@ nosa_status nosa_attend(const nosa_config* cfg, const nosa_state* st, const uint
  * computes exactly what nosa_decode_attn computes but takes no workspace: its scratch (the
  * split-K partials and the per-group counters) lives in a static device array of 8 MiB
  * inside the library, which every GPU that loads the library keeps until the process exits.
- * Limit: B*Hkv * (16 * G * (d + 2) * 4 bytes, rounded up to 256) plus B*Hkv * 4 bytes must
+ * Limit: B*Hkv * (16 * G * (d + 2) * 4 bytes, rounded up to 256; with kv_bits = 4 the 2 * G
+ * floats beside the G * d are rounded up to 4) plus B*Hkv * 4 bytes must
  * fit in 8 MiB (about 250 groups at G = 4, d = 128); larger configurations get NOSA_ENOMEM and
  * must use nosa_decode_attn with a workspace. Allocates nothing: no cudaMalloc, no cudaFree.
  * The first call on each device looks up the array's device address (cudaGetSymbolAddress)

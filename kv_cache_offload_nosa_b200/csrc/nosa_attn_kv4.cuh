@@ -1,11 +1,18 @@
 // Split-K flash-decoding over the selected blocks of a 4-bit cache (kv_bits = 4).
 //
-// The tasks, their split over CTAs and the merge of the partials are those of the bf16 kernel:
-// the B*Hkv*k (group, selected block) tasks, group after group, are cut in ranges of W, one range
-// per CTA (or each group in ranges of its own); each range writes one partial (m, l, acc) per query head and group it touches, and the
-// last CTA to finish a group (atomic ticket) merges them. One producer warp brings each task's K
-// and V page (two bulk copies, codes and scales together) into a ring of stages; the consumer warps
-// take 32 tokens each, a page's units going to neighbouring warps and page after page to the next.
+// The tasks and the merge of the partials are those of the bf16 kernel: the B*Hkv*k (group, selected
+// block) tasks, group after group, are cut in ranges of W, one range per CTA (or each group in ranges
+// of its own); each range writes one partial (m, l, acc) per query head and group it touches, and the
+// last CTA to finish a group (atomic ticket) merges them. One producer warp brings each task's K and V
+// page (two bulk copies, codes and scales together) into a ring of stages; the consumer warps take 32
+// tokens each, a page's units going to neighbouring warps and page after page to the next.
+//
+// Bound: the pages are 3.6 times smaller than bf16 ones, so unpacking them bounds the kernel before
+// memory does. Per 16 tokens (d = 128) a warp issues about 370 instructions, 146 of them on the integer
+// pipe (two cycles each). Over four sequences of 131072 tokens, 8 KV heads of 4 query heads each, it
+// takes 149 us (4.0 TB/s; the same pages copied and not unpacked: 97 us); what counts is instructions,
+// not warps (8 or 12 consumer warps an SM take the same time). mma.sync and not tcgen05: a group has
+// G <= 8 query rows, and codes have to pass through registers on their way to an operand.
 //
 // The pages are never expanded. With s the scales and c the codes,
 //   score:  sum_d q_d K_td = sum_g s_tg sum_{d in g} q_d (c_td - 8),
@@ -238,7 +245,8 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
 
 // WIDE: more than four query heads a group.
 template <int D, int BS, bool WIDE>
-__global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, BS>::CTAS) attn_kv4_kernel(AttnKv4Args x) {
+__global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, BS>::CTAS)
+    attn_kv4_kernel(AttnKv4Args x) {
   using SH = AttnKv4Shape<D, BS>;
   constexpr int NC = SH::NC, U = SH::U;
   constexpr int NG = D / 32;  // groups of a row
@@ -248,11 +256,11 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   const int ST = a.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kKv4MaxStages;
-  int2* info = reinterpret_cast<int2*>(empty + kKv4MaxStages);         // a stage's block (-1: none) and length
+  int2* info = reinterpret_cast<int2*>(empty + kKv4MaxStages);  // a stage's block (-1: none) and length
   uint64_t* meet = reinterpret_cast<uint64_t*>(info + kKv4MaxStages);  // the consumer warps' meeting point
   int* s_flag = reinterpret_cast<int*>(meet + 1);
-  uint4* sq = reinterpret_cast<uint4*>(meet + 2);              // [NG][32] a lane's q operands of a group
-  float* scr = reinterpret_cast<float*>(sq + NG * 32);          // [NC] partials at a merge
+  uint4* sq = reinterpret_cast<uint4*>(meet + 2);       // [NG][32] a lane's q operands of a group
+  float* scr = reinterpret_cast<float*>(sq + NG * 32);  // [NC] partials at a merge
   float4* sums = reinterpret_cast<float4*>(scr) + warp_id() * NG * 2 * 32;  // this warp's sums, between merges
   uint8_t* stages = smem + SH::template FIXED<WIDE ? 8 : 4> - 128;
 
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     // ---------------------------------------------------------------- producer
     // As the bf16 kernel's: ranges cut at group boundaries, taken in parts that wait for the same
     // flag (a group's query-agnostic blocks may be ready before the rest of its selection); 32
-    // tasks' pages are looked up at once, lane 0 issues the copies in task order.
+    // tasks' pages are looked up at once, and their copies issued by a lane each.
     const bool early = a.att_list != nullptr;
     const int32_t* list = early ? a.att_list : a.sel;
     int it = 0, s = 0, round = 0;  // next task, its stage, and how often the ring has gone round
@@ -338,7 +346,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
             }
             bool free = lane < min(round == 0 ? SH::STEP : ST, nb - v);
             if (free && rl > 0)
-              free = lane < SH::STEP ? mbar_wait(&empty[sl], (rl - 1) & 1, deadline) : mbar_test(&empty[sl], (rl - 1) & 1);
+              free = lane < SH::STEP ? mbar_wait(&empty[sl], (rl - 1) & 1, deadline)
+                                     : mbar_test(&empty[sl], (rl - 1) & 1);
             const int n = __ffs(~__ballot_sync(0xffffffffu, free)) - 1;  // (32 of them: ~0 has no bit)
             const int cnt = n < 0 ? 32 : n;
             if (cnt == 0) {
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     // never leave the CTA with a copy in flight
     if (lane < min(ST, it)) {
       const int i = it - 1 - lane;
-      mbar_wait(&full[i % ST], (i / ST) & 1, abort ? globaltimer() + a.wait_ns : deadline);
+      mbar_wait(&full[i % ST], (i / ST) & 1, globaltimer() + a.wait_ns);
     }
     return;
   }
@@ -383,9 +392,9 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   // ---------------------------------------------------------------- consumers
   // S^T = K . q^T: rows are tokens, columns heads. Row i < 8 of a tile of 16 is token
   // (i >> 1) + 4 (i & 1) and row i + 8 that plus 8: lane c4 of the second product then takes tokens
-  // c4, c4 + 4, c4 + 8 and c4 + 12, whose V rows lie in different banks. With G <= 4 column h + 4
-  // repeats head h and carries the low parts of its weights; with G = 8 the low parts take a second
-  // product. Columns without a head have q = 0 and are not written.
+  // c4, c4 + 4, c4 + 8 and c4 + 12, neighbouring rows in one load (two bank conflicts, not four). With
+  // G <= 4 column h + 4 repeats head h and carries the low parts of its weights; with G = 8 the low
+  // parts take a second product. Columns without a head have q = 0 and are not written.
   const int r = lane >> 2, c4 = lane & 3;
   auto col_head = [&](int n) { return WIDE ? n : (n & 3); };
   const float lo_sign = (!WIDE && c4 >= 2) ? -1.f : 0.f;  // low columns take w - fp16(w)
@@ -752,7 +761,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
         return;
       }
       if (*s_flag) {
-        if (!kv4_merge<D, NC, WIDE>(a.partials + (size_t)gi * x.pslots * GE, outg, scr, nseg, a.G, meet, met, deadline)) {
+        if (!kv4_merge<D, NC, WIDE>(a.partials + (size_t)gi * x.pslots * GE, outg, scr, nseg, a.G, meet, met,
+                                    deadline)) {
           set_err(a.err, NOSA_ERR_TIMEOUT);
           return;
         }

@@ -25,7 +25,6 @@
 
 namespace nosa {
 
-__host__ __device__ constexpr int kv4_row_bytes(int d) { return d / 2; }
 __host__ __device__ constexpr int kv4_page_bytes(int bs, int d) { return bs * (d / 2 + d / 16); }
 
 // bf16 bits of the scale of a group whose largest magnitude has the bf16 bits `amax`. The product
@@ -247,7 +246,8 @@ __global__ void __launch_bounds__(256, 6) kv4_read_kernel(KvRunArgs a) {
       const uint8_t* kp = a.k_pages + at.x * PB;
       const uint8_t* vp = a.v_pages + at.x * PB;
       kw[u] = __ldcs(reinterpret_cast<const uint32_t*>(kp + at.y * (D / 2) + c * (D / 8) + 4 * g));
-      vw[u] = __ldcs(reinterpret_cast<const uint32_t*>(vp + at.y * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)));
+      vw[u] = __ldcs(
+          reinterpret_cast<const uint32_t*>(vp + at.y * (D / 2) + (2 * c + odd) * (D / 16) + 4 * (g >> 1)));
       ks[u] = __ldcs(reinterpret_cast<const uint16_t*>(kp + a.bs * (D / 2) + at.y * (D / 16)) + g);
       vs[u] = __ldcs(reinterpret_cast<const uint16_t*>(vp + a.bs * (D / 2) + at.y * (D / 16)) + g);
     }
