@@ -137,10 +137,14 @@ def _stream(stream) -> Optional[int]:
         global _raw_stream
         if _raw_stream is None:
             import torch
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            # the handle alone, without building a Stream object for each call (3 us)
-            _raw_stream = ((lambda: raw(torch.cuda.current_device())) if raw
-                           else (lambda: torch.cuda.current_stream().cuda_stream))
+            c = torch._C
+            if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+                # the handle alone, without building a Stream object for each call (3 us)
+                raw, dev = c._cuda_getCurrentRawStream, c._cuda_getDevice
+                torch.cuda.current_stream()  # the device is set up
+                _raw_stream = lambda: raw(dev())
+            else:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
         return _raw_stream()
     if isinstance(stream, int):
         return stream

@@ -58,20 +58,24 @@ def check_run(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor, cu_tokens, sta
     """Refuses (NosaError, NOSA_EINVAL) what is not a run of tokens on `device`: k and v
     [n_tokens, Hkv, d] of 16-bit values with contiguous rows, cu_tokens [B + 1] and start [B]
     (or None) int32 and contiguous. Returns the rows' strides, None where both are contiguous."""
-    want, index = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d), device.index
-    for name, t in (("k", k), ("v", v)):
-        if t.get_device() != index:
-            raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
-        if t.dtype not in _ROW_TYPES:
-            raise NosaError(NOSA_EINVAL, f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
-        if t.shape != want:
-            raise NosaError(NOSA_EINVAL, f"{name} must be {list(want)}, not {list(t.shape)}")
-    for name, t, n in (("cu_tokens", cu_tokens, cfg.B + 1), ("start", start, cfg.B)):
+    index, B, i32 = device.index, cfg.B, torch.int32
+    want = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d)
+    if not (k.shape == want and v.shape == want and k.dtype in _ROW_TYPES and v.dtype in _ROW_TYPES and
+            k.get_device() == index and v.get_device() == index):
+        for name, t in (("k", k), ("v", v)):
+            if t.get_device() != index:
+                raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
+            if t.dtype not in _ROW_TYPES:
+                raise NosaError(NOSA_EINVAL,
+                                f"{name} must hold bf16 values (or their 16-bit patterns), not {t.dtype}")
+            if t.shape != want:
+                raise NosaError(NOSA_EINVAL, f"{name} must be {list(want)}, not {list(t.shape)}")
+    for name, t, n in (("cu_tokens", cu_tokens, B + 1), ("start", start, B)):
         if t is None and name == "start":
             continue
         if t.get_device() != index:
             raise NosaError(NOSA_EINVAL, f"{name} is on {t.device}, the state is on {device}")
-        if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
+        if t.dtype is not i32 or t.numel() < n or not t.is_contiguous():
             raise NosaError(NOSA_EINVAL, f"{name} must be {n} contiguous int32 values, not {t.dtype} {list(t.shape)}")
     if k.is_contiguous() and v.is_contiguous():
         return None

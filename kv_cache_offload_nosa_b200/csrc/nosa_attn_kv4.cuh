@@ -158,7 +158,8 @@ __device__ __forceinline__ bool kv4_meeting(uint64_t* meet, uint32_t met, unsign
 }
 
 // The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' factors (a
-// head per warp, a segment per lane), then every NC-th segment per warp, the warps' sums last. scr:
+// head per warp, a segment per lane) with the first values under way, then every NC-th segment per
+// warp, the warps' sums last. scr:
 // shared memory for [G] x 128 factors, [G] sums and [NC][G][D] values. Two meetings. Out of line: its
 // registers would cost the main loop.
 template <int D, int NC, bool WIDE>
@@ -168,6 +169,21 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
   float* fac = scr;
   float* den = scr + G * kKv4MaxSlots;
   float4* add = reinterpret_cast<float4*>(den + ((G + 3) & ~3));
+  constexpr int E = (WIDE ? 8 : 4) * D / 128;  // four values of a head each, 32 apart
+  constexpr int AT = 8 / E;                    // segments in flight
+  const int ne = G * (D / 4);
+  float4 y[AT][E];
+  auto load = [&](int sg) {
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        y[t][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (sg + t * NC < nseg && lane + 32 * i < ne)
+          y[t][i] = __ldcg(reinterpret_cast<const float4*>(p0 + (size_t)(sg + t * NC) * GE) + lane + 32 * i);
+      }
+  };
+  load(warp);
   for (int h = warp; h < G; h += NC) {
     float2 ml[kKv4MaxSlots / 32];
     float M = -INFINITY, L = 0.f;
@@ -194,22 +210,11 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
     if (lane == 0) den[h] = L;
   }
   if (!kv4_meeting(meet, met, deadline)) return false;
-  constexpr int E = (WIDE ? 8 : 4) * D / 128;  // four values of a head each, 32 apart
-  constexpr int AT = 8 / E;                    // segments in flight
-  const int ne = G * (D / 4);
   float4 v[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int sg = warp; sg < nseg; sg += AT * NC) {
-    float4 y[AT][E];
-#pragma unroll
-    for (int t = 0; t < AT; ++t)
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        y[t][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (sg + t * NC < nseg && lane + 32 * i < ne)
-          y[t][i] = __ldcg(reinterpret_cast<const float4*>(p0 + (size_t)(sg + t * NC) * GE) + lane + 32 * i);
-      }
+    if (sg != warp) load(sg);
 #pragma unroll
     for (int t = 0; t < AT; ++t)
 #pragma unroll
@@ -746,15 +751,18 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       if (tid == 0) clear_flags(gi);
     } else {
       // The last CTA to publish its part (atomic ticket, no spinning) merges the group. One thread's
-      // fences stand for the CTA's: the meetings order the others before and after it.
+      // release and acquire stand for the CTA's: the meetings order the others before and after it.
       if (!meeting()) {
         set_err(a.err, NOSA_ERR_TIMEOUT);
         return;
       }
       if (tid == 0) {
-        __threadfence();
-        *s_flag = atomicAdd(&a.counters[gi], 1u) == (unsigned)(nseg - 1);
-        __threadfence();
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(&a.counters[gi])
+                     : "memory");
+        *s_flag = before == (unsigned)(nseg - 1);
       }
       if (!meeting()) {
         set_err(a.err, NOSA_ERR_TIMEOUT);
