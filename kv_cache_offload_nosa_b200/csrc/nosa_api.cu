@@ -421,13 +421,13 @@ int attn_split_for(int split, int k, int total, long long target, int sms, int s
 
 // The same for 4-bit pages. Unpacking bounds the kernel, and the CTAs of an SM share its issue slots,
 // so an even load counts: every CTA that the GPU holds at once gets the same number of tasks, wherever
-// that cuts a group (2048 blocks of 64 tokens, 32 groups, d = 128, 444 CTAs: 144 us in even shares of
-// 148, 149 us in ranges of 158 within the groups, 172 us in ranges of 128). But a CTA with parts of two
+// that cuts a group (2048 blocks of 64 tokens, 32 groups, d = 128, 444 CTAs: 147 us in even shares of
+// 148, 153 us in ranges of 158 within the groups, 180 us in ranges of 128). But a CTA with parts of two
 // groups starts and ends a part twice, about 3 us. Ranges within the groups (parts > 0) are taken where
 // they leave no SM more than 96 Ki values of K rows over the even share, which is what it unpacks in
-// that time (64 blocks, 128 groups: 30.4 against 31.2 us; 2048 blocks, 8 groups: 47.6 against 50.4 us;
-// 77 blocks of 32 tokens, 128 groups, d = 64: 15.1 against 17.4 us). With fewer than about two CTAs an
-// SM nothing covers their latencies (the last case with one range a group: 18.5 us).
+// that time (64 blocks, 128 groups: 29.4 against 30.4 us; 2048 blocks, 8 groups: 48.0 against 49.7 us;
+// 77 blocks of 32 tokens, 128 groups, d = 64: 14.4 against 16.7 us). With fewer than about two CTAs an
+// SM nothing covers their latencies (the last case with one range a group: 17.7 us).
 // finest: ranges within the groups too, up to 16 each.
 struct Kv4Split {
   int W, parts, ctas;

@@ -10,7 +10,7 @@
 // Bound: the pages are 3.6 times smaller than bf16 ones, so unpacking them bounds the kernel before
 // memory does. Per 16 tokens (d = 128) a warp issues about 370 instructions, 146 of them on the integer
 // pipe (two cycles each). Over four sequences of 131072 tokens, 8 KV heads of 4 query heads each, it
-// takes 149 us (4.0 TB/s; the same pages copied and not unpacked: 97 us); what counts is instructions,
+// takes 147 us (4.1 TB/s; the same pages copied and not unpacked: 97 us); what counts is instructions,
 // not warps (8 or 12 consumer warps an SM take the same time). mma.sync and not tcgen05: a group has
 // G <= 8 query rows, and codes have to pass through registers on their way to an operand.
 //
