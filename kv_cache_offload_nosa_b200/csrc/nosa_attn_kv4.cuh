@@ -447,8 +447,9 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 2^e takes the largest there; e is kept where 2^e and 2^-e are floats
-      const int e = min(max(140 - static_cast<int>(mx >> 7), -100), 100);
+      // 2^e takes the largest there: any finite q down to 2^-87; below, e stays at 100, so that sums of
+      // up to 2^24 times a score are floats, and q loses digits
+      const int e = min(max(140 - static_cast<int>(mx >> 7), -114), 100);
       const float up = __uint_as_float((127 + e) << 23);
       const float fq = __uint_as_float((127 - e) << 23) * a.scale_log2;
       // from column r of B (all four c4 lanes agree) to columns 2 c4, 2 c4 + 1 of C

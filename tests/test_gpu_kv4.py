@@ -326,7 +326,8 @@ def test_attention(d, bs, G, Hkv, lens, k, split):
     assert cache.check() == (nosa.NOSA_OK, 0)
 
 
-@pytest.mark.parametrize("qs,ks,vs", [(30.0, 1.0, 1.0), (1e-6, 1.0, 1e-6), (1e4, 1e-4, 1e6), (1.0, 3e4, 1e-12), (1e-20, 1e20, 1e18)])
+@pytest.mark.parametrize("qs,ks,vs", [(30.0, 1.0, 1.0), (1e-6, 1.0, 1e-6), (1e4, 1e-4, 1e6), (1.0, 3e4, 1e-12), (1e-20, 1e20, 1e18),
+                                      (1e36, 1e-36, 1.0), (1e-25, 1e25, 1.0)])
 def test_attention_over_wide_ranges(qs, ks, vs):
     """Queries, keys and values far from 1: weights sharp or flat, values large and small."""
     rng = np.random.default_rng(77)
