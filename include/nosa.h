@@ -190,7 +190,7 @@ nosa_status nosa_state_init(const nosa_config* cfg, const nosa_state* st, const 
  * clears the error word (call nosa_check_device before it to see a write's fault). Reading is the
  * same call with k and v as outputs, rounded to nearest even (a value within 2^-8 of the largest
  * bf16 may come back as infinity), from the same pools; rows must not overlap. n_tokens * Hkv
- * < 2^30.
+ * < 2^30; a run of no tokens does nothing (k, v and cu_tokens may be NULL).
  */
 typedef struct nosa_kv_strides {
   int64_t k_tok, k_head, v_tok, v_head;

@@ -785,6 +785,11 @@ nosa_status kv_run_args(const nosa_config* cfg, const nosa_state* st, const uint
   NOSA_CHECK(kv4(c), "kv_bits = %d: runs of tokens are written to and read from 4-bit caches", c.kv_bits);
   NOSA_CHECK(n_tokens >= 0 && (long long)n_tokens * c.Hkv < (1ll << 30), "n_tokens = %d not in [0, 2^30 / Hkv)",
              n_tokens);
+  if (n_tokens == 0) {  // an empty run has no rows, and may have no memory
+    a->n_tokens = 0;
+    a->Hkv = c.Hkv;
+    return NOSA_OK;
+  }
   NOSA_CHECK(k && v && cu_tokens && aligned16(k) && aligned16(v) && aligned16(cu_tokens) && aligned16(start),
              "k/v/cu_tokens NULL or misaligned");
   const long long tok = (long long)c.Hkv * c.d;

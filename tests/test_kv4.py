@@ -113,6 +113,7 @@ def test_an_empty_run_launches_nothing(lib):
     c, st = cfg(), state()
     for f in (lib.nosa_write_kv, lib.nosa_read_kv):
         assert f(ctypes.byref(c), ctypes.byref(st), 0x100000, 0x200000, None, 0, 0x300000, None, None) == nosa.NOSA_OK
+        assert f(ctypes.byref(c), ctypes.byref(st), None, None, None, 0, None, None, None) == nosa.NOSA_OK
 
 
 @pytest.mark.parametrize("bits", [0, 16])
