@@ -583,6 +583,7 @@ template <int D, int BS, bool WIDE>
 nosa_status launch_attn_kv4_t(const nosa_config& c, AttnKv4Args x, cudaStream_t s, bool finest, bool pdl) {
   using SH = AttnKv4Shape<D, BS>;
   constexpr int GM = WIDE ? 8 : 4, smem = SH::template SMEM<GM>, ctas = SH::template ctas_per_sm<GM>();
+  static_assert(SH::template stages<GM>() % SH::STEP == 0, "every warp has to come to its stages in each round");
   auto k = attn_kv4_kernel<D, BS, WIDE>;
   int dev = 0, sms = 0;
   NOSA_CUDA(cudaGetDevice(&dev));

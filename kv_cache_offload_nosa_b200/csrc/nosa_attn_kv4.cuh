@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
           __syncwarp();
         }
         if (!early) L = __ldcg(a.seq_len + gi);
-        if (flags && lane == 0) fence_proxy_async_global();  // pages written before the flags
+        if (flags) fence_proxy_async_global();  // pages written before the flags; every lane copies
         const int N = (L + BS - 1) / BS;
         for (int base = p; base < pend && !abort; base += 32) {
           const int p_l = base + lane;
