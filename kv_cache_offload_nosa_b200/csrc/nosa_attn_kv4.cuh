@@ -159,9 +159,8 @@ __device__ __forceinline__ bool kv4_meeting(uint64_t* meet, uint32_t met, unsign
 
 // The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' factors (a
 // head per warp, a segment per lane) with the first values under way, then every NC-th segment per
-// warp, the warps' sums last. scr:
-// shared memory for [G] x 128 factors, [G] sums and [NC][G][D] values. Two meetings. Out of line: its
-// registers would cost the main loop.
+// warp, the warps' sums last. scr: shared memory for [G] x 128 factors, [G] sums and [NC][G][D] values.
+// Two meetings. Out of line: its registers would cost the main loop.
 template <int D, int NC, bool WIDE>
 __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr, int nseg, int G, uint64_t* meet,
                                        uint32_t met, unsigned long long deadline) {
