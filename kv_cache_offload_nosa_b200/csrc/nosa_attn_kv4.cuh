@@ -2,10 +2,11 @@
 //
 // The tasks and the merge of the partials are those of the bf16 kernel: the B*Hkv*k (group, selected
 // block) tasks, group after group, are cut in ranges of W, one range per CTA (or each group in ranges
-// of its own); each range writes one partial (m, l, acc) per query head and group it touches, and the
-// last CTA to finish a group (atomic ticket) merges them. One producer warp brings each task's K and V
-// page (two bulk copies, codes and scales together) into a ring of stages; the consumer warps take 32
-// tokens each, a page's units going to neighbouring warps and page after page to the next.
+// of its own); each range writes one partial per query head and group it touches (the mean of V under
+// its weights, and their sum as l 2^m), and the last CTA to finish a group (atomic ticket) merges them.
+// One producer warp brings each task's K and V page (two bulk copies, codes and scales together) into a
+// ring of stages; the consumer warps take 32 tokens each, a page's units going to neighbouring warps and
+// page after page to the next.
 //
 // Bound: the pages are 3.6 times smaller than bf16 ones, so unpacking them bounds the kernel before
 // memory does. Per 16 tokens (d = 128) a warp issues about 370 instructions, 146 of them on the integer
@@ -41,7 +42,7 @@ namespace nosa {
 constexpr int kKv4MaxStages = 16;
 constexpr int kKv4MaxSlots = 128;  // partial slots per group, at most
 
-// Floats of one partial slot: acc [G][D], then (m, l) [G], in 16-byte steps.
+// Floats of one partial slot: means [G][D], then (m, l) [G], in 16-byte steps.
 __host__ __device__ constexpr int kv4_part_floats(int G, int D) { return G * D + ((2 * G + 3) & ~3); }
 
 struct AttnKv4Args {
@@ -69,7 +70,7 @@ struct AttnKv4Shape {
   template <int GM>
   static constexpr int FIXED =
       128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * 512 +
-      most(NC * D * 8 * 4, most(NC * kv4_part_floats(GM, D), GM * kKv4MaxSlots + GM + NC * GM * D) * 4);
+      most(NC * D * 8 * 4, most(NC * kv4_part_floats(GM, D), GM * kKv4MaxSlots + NC * GM * D) * 4);
   // As many stages as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
   template <int GM>
   static constexpr int stages() {
@@ -157,17 +158,22 @@ __device__ __forceinline__ bool kv4_meeting(uint64_t* meet, uint32_t met, unsign
   return __all_sync(0xffffffffu, mbar_wait(meet, met & 1u, deadline));
 }
 
-// The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' factors (a
-// head per warp, a segment per lane) with the first values under way, then every NC-th segment per
-// warp, the warps' sums last. scr: shared memory for [G] x 128 factors, [G] sums and [NC][G][D] values.
+// The square root of the factor that takes sums from the reference `from` to `to`, the larger one.
+// References hold the scales of V, so that they may lie 220 apart while the scores do not: the factor
+// itself would be zero below 2^-126, where an l of up to 2^103 and more still counts; it is applied to l
+// in two halves. (The sums of V are at most 2^15 a weight at any reference, so that theirs may vanish.)
+__device__ __forceinline__ float half_factor(float from, float to) { return from == to ? 1.f : ex2(0.5f * (from - to)); }
+
+// The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' shares of the
+// weights (a head per warp, a segment per lane) with the first values under way, then every NC-th
+// segment per warp, the warps' sums last. scr: shared memory for [G] x 128 shares and [NC][G][D] values.
 // Two meetings. Out of line: its registers would cost the main loop.
 template <int D, int NC, bool WIDE>
 __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr, int nseg, int G, uint64_t* meet,
                                        uint32_t met, unsigned long long deadline) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, GE = kv4_part_floats(G, D);
-  float* fac = scr;
-  float* den = scr + G * kKv4MaxSlots;
-  float4* add = reinterpret_cast<float4*>(den + ((G + 3) & ~3));
+  float* share = scr;
+  float4* add = reinterpret_cast<float4*>(scr + G * kKv4MaxSlots);
   constexpr int E = (WIDE ? 8 : 4) * D / 128;  // four values of a head each, 32 apart
   constexpr int AT = 8 / E;                    // segments in flight
   const int ne = G * (D / 4);
@@ -197,16 +203,16 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
     for (int i = 0; i < kKv4MaxSlots / 32; ++i) {
-      const int sg = 32 * i + lane;
-      const float f = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
-      if (sg < nseg) {
-        L = fmaf(ml[i].y, f, L);
-        fac[h * kKv4MaxSlots + sg] = f;
-      }
+      const float f = half_factor(ml[i].x, M);
+      ml[i].y = ml[i].y * f * f;
+      L += ml[i].y;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) den[h] = L;
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (no token at all)
+#pragma unroll
+    for (int i = 0; i < kKv4MaxSlots / 32; ++i)
+      if (32 * i + lane < nseg) share[h * kKv4MaxSlots + 32 * i + lane] = ml[i].y * inv;
   }
   if (!kv4_meeting(meet, met, deadline)) return false;
   float4 v[E];
@@ -219,7 +225,7 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int h = min((lane + 32 * i) / (D / 4), G - 1);
-        const float f = fac[h * kKv4MaxSlots + min(sg + t * NC, nseg - 1)];
+        const float f = share[h * kKv4MaxSlots + min(sg + t * NC, nseg - 1)];
         v[i].x = fmaf(y[t][i].x, f, v[i].x);
         v[i].y = fmaf(y[t][i].y, f, v[i].y);
         v[i].z = fmaf(y[t][i].z, f, v[i].z);
@@ -240,9 +246,7 @@ __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr,
       y.z += z.z;
       y.w += z.w;
     }
-    const float L = den[e / (D / 4)], inv = 1.f / L;
-    reinterpret_cast<float4*>(outg)[e] = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)  // no token at all
-                                                  : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    reinterpret_cast<float4*>(outg)[e] = y;
   }
   return true;
 }
@@ -593,11 +597,12 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
               }
             y0 = y1 = -INFINITY;
           }
-          const float al0 = mn0 == m0 ? 1.f : ex2(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2(m1 - mn1);
+          const float hf0 = half_factor(m0, mn0), hf1 = half_factor(m1, mn1);
+          const float al0 = hf0 * hf0, al1 = hf1 * hf1;
           m0 = mn0;
           m1 = mn1;
-          l0 *= al0;
-          l1 *= al1;
+          l0 = l0 * hf0 * hf0;
+          l1 = l1 * hf1 * hf1;
 #pragma unroll
           for (int mt = 0; mt < 2 * NG; ++mt) {
             acc[mt][0] *= al0;
@@ -719,32 +724,32 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     float* outg = a.out + ((size_t)(gi / a.Hkv) * a.Hq + (gi % a.Hkv) * a.G) * D;
 #pragma unroll 1
     for (int e = tid; e < a.G * (D / 4); e += NC * 32) {
-      const int h = e / (D / 4);
+      const int head = e / (D / 4);
       float2 ml[NC];
       float M = -INFINITY, L = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < NC; ++w) {
-        ml[w] = reinterpret_cast<const float2*>(scr + w * GE + a.G * D)[h];
+        ml[w] = reinterpret_cast<const float2*>(scr + w * GE + a.G * D)[head];
         M = fmaxf(M, ml[w].x);
       }
 #pragma unroll
       for (int w = 0; w < NC; ++w) {
-        const float f = ml[w].x == M ? 1.f : ex2(ml[w].x - M);
+        const float h = half_factor(ml[w].x, M), f = h * h;
         const float4 y = reinterpret_cast<const float4*>(scr + w * GE)[e];
-        L = fmaf(ml[w].y, f, L);
+        L = fmaf(ml[w].y * h, h, L);
         v.x = fmaf(y.x, f, v.x);
         v.y = fmaf(y.y, f, v.y);
         v.z = fmaf(y.z, f, v.z);
         v.w = fmaf(y.w, f, v.w);
       }
+      const float inv = L == 0.f ? 0.f : 1.f / L;  // (no token at all: zeros)
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       if (nseg == 1) {
-        const float inv = 1.f / L;
-        reinterpret_cast<float4*>(outg)[e] = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)  // no token at all
-                                                      : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        reinterpret_cast<float4*>(outg)[e] = v;
       } else {
         reinterpret_cast<float4*>(part)[e] = v;
-        if (e % (D / 4) == 0) reinterpret_cast<float2*>(part + a.G * D)[h] = make_float2(M, L);
+        if (e % (D / 4) == 0) reinterpret_cast<float2*>(part + a.G * D)[head] = make_float2(M, L);
       }
     }
     if (nseg == 1) {
