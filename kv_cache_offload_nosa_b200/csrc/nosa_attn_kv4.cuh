@@ -30,6 +30,8 @@
 // exceeds it by more than 13. Weights are thus below 2^15, and one of 2^-14 of the largest still
 // has all 22 bits of its two parts. (e_t is at least -90, which keeps p and its sum finite: V below
 // 2^-100 loses digits, and below 2^-120 vanishes. Above 2^112 weights under 2^-11 of the largest do.)
+// Beyond 2^20 a score plus e_t is not e_t precise enough, and a warp that meets one there carries its
+// references as pairs a + b: a near the scores and taken from them first, b for the scales of V.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,6 +43,7 @@ namespace nosa {
 
 constexpr int kKv4MaxStages = 16;
 constexpr int kKv4MaxSlots = 128;  // partial slots per group, at most
+constexpr float kKv4None = -0x1.fffffep127f;  // the reference where no token has been seen
 
 // Floats of one partial slot: means [G][D], then (m, l) [G], in 16-byte steps.
 __host__ __device__ constexpr int kv4_part_floats(int G, int D) { return G * D + ((2 * G + 3) & ~3); }
@@ -65,11 +68,11 @@ struct AttnKv4Shape {
   static constexpr int PAGE = kv4_page_bytes(BS, D);
   static constexpr int STAGE = 2 * PAGE;
   static constexpr int most(int a, int b) { return a > b ? a : b; }
-  // Shared memory for up to GM query heads a group: alignment, barriers, tasks, meeting point, q; what
-  // the sums, the warps' partials and the merge share; the stages.
+  // Shared memory for up to GM query heads a group: alignment, barriers, tasks, meeting point, q, the
+  // warps' pairs; what the sums, the warps' partials and the merge share; the stages.
   template <int GM>
   static constexpr int FIXED =
-      128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * 512 +
+      128 + kKv4MaxStages * (8 + 8 + 8) + 16 + (D / 32) * 512 + NC * 128 +
       most(NC * D * 8 * 4, most(NC * kv4_part_floats(GM, D), GM * kKv4MaxSlots + NC * GM * D) * 4);
   // As many stages as the CTAs of an SM leave room for, a multiple of STEP, at least two pages.
   template <int GM>
@@ -268,7 +271,9 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
   uint64_t* meet = reinterpret_cast<uint64_t*>(info + kKv4MaxStages);  // the consumer warps' meeting point
   int* s_flag = reinterpret_cast<int*>(meet + 1);
   uint4* sq = reinterpret_cast<uint4*>(meet + 2);       // [NG][32] a lane's q operands of a group
-  float* scr = reinterpret_cast<float*>(sq + NG * 32);  // [NC] partials at a merge
+  // [NC][4] of a lane column's two heads: (a, a, b, b) of the pairs, and the factors of the scores
+  float4* pairs = reinterpret_cast<float4*>(sq + NG * 32);
+  float* scr = reinterpret_cast<float*>(pairs + NC * 8);  // [NC] partials at a merge
   float4* sums = reinterpret_cast<float4*>(scr) + warp_id() * NG * 2 * 32;  // this warp's sums, between merges
   uint8_t* stages = smem + SH::template FIXED<WIDE ? 8 : 4> - 128;
 
@@ -474,8 +479,12 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     float acc[2 * NG][4];
 #pragma unroll
     for (int mt = 0; mt < 2 * NG; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-    // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0)
-    float m0 = -INFINITY, m1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // m: reference of the weights; y: what x + e may reach before m moves (offset by Y0). With pairs
+    // m = 0 and f = 1, the pair goes off the scores as they come, and y stays at -inf, so that it does.
+    float m0 = kKv4None, m1 = kKv4None, y0 = -INFINITY, y1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    auto paired = [&]() -> bool {
+      return __any_sync(0xffffffffu, (y0 == -INFINITY && m0 != kKv4None) || (y1 == -INFINITY && m1 != kKv4None));
+    };
     // The tensor cores truncate as they add: an error of about 2^-24 a step, all one way. Every
     // 16 units the accumulators go to sums in shared memory, held relative to (r0, r1).
     float r0 = -INFINITY, r1 = -INFINITY;
@@ -548,18 +557,21 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
                 for (int g = 0; g < NG / 2; ++g) sv[t][b][g] = 0u;
               }
         }
-        // The bf16 bits of a scale, as an integer over 128, are its base-2 logarithm plus 127 within
-        // 0.09. 0x4b000000 + bits is 2^23 + bits as a float: over 128 that is Y0 + e. (e is at least
-        // -90, so that 2^-e and sums of it stay finite.)
+        // Y0 + e of a token. The bf16 bits of a scale, as an integer over 128, are its base-2 logarithm
+        // plus 127 within 0.09. 0x4b000000 + bits is 2^23 + bits as a float: over 128 that is Y0 + e. (e is
+        // at least -90, so that 2^-e and sums of it stay finite.)
+        auto top_exponent = [&](const uint32_t* scales) {
+          float top = 0x1p-90f;
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) top = fmaxf(top, fmaxf(bf16_lo(scales[g]), bf16_hi(scales[g])));
+          return 0x1p-7f * __uint_as_float(__byte_perm(__float_as_uint(top), 0x4b000000u, 0x7632));
+        };
         float yn0 = -INFINITY, yn1 = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            float top = 0x1p-90f;
-#pragma unroll
-            for (int g = 0; g < NG / 2; ++g) top = fmaxf(top, fmaxf(bf16_lo(sv[t][b][g]), bf16_hi(sv[t][b][g])));
-            const float e = 0x1p-7f * __uint_as_float(__byte_perm(__float_as_uint(top), 0x4b000000u, 0x7632));
+            const float e = top_exponent(sv[t][b]);
             yn0 = fmaxf(yn0, fmaf(xs[t][b][0], f0, e));
             yn1 = fmaxf(yn1, fmaf(xs[t][b][1], f1, e));
           }
@@ -569,38 +581,84 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
             yn0 = fmaxf(yn0, __shfl_xor_sync(0xffffffffu, yn0, o));
             yn1 = fmaxf(yn1, __shfl_xor_sync(0xffffffffu, yn1, o));
           }
-          float mn0 = fmaxf(m0, yn0 - (Y0 + 10.f)), mn1 = fmaxf(m1, yn1 - (Y0 + 10.f));
-          // scores so large that a sum with e says little: from here on (y stays -inf) m is the
-          // largest score, found for every unit, and subtracted here
-          const bool huge = (y0 == -INFINITY && m0 != -INFINITY) || (y1 == -INFINITY && m1 != -INFINITY) ||
-                            fabsf(yn0) > 0x1p20f || fabsf(yn1) > 0x1p20f;
-          y0 = fmaxf(y0, yn0 + 3.f);
-          y1 = fmaxf(y1, yn1 + 3.f);
-          if (__any_sync(0xffffffffu, huge)) {
-            mn0 = fmaxf(fmaxf(xs[0][0][0], xs[0][1][0]), fmaxf(xs[1][0][0], xs[1][1][0]));
-            mn1 = fmaxf(fmaxf(xs[0][0][1], xs[0][1][1]), fmaxf(xs[1][0][1], xs[1][1][1]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              mn0 = fmaxf(mn0, __shfl_xor_sync(0xffffffffu, mn0, o));
-              mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
-            }
-            mn0 = fmaxf(m0, __fmul_rn(mn0, f0));
-            mn1 = fmaxf(m1, __fmul_rn(mn1, f1));
-            // x - m with x rounded as m was (the fused form below would keep what m lost)
-            const float z0 = mn0 == -INFINITY ? 0.f : mn0, z1 = mn1 == -INFINITY ? 0.f : mn1;
+          float hf0, hf1;
+          const bool were = paired();
+          if (!__any_sync(0xffffffffu, were || fabsf(yn0 == -INFINITY ? 0.f : yn0) > 0x1p20f ||
+                                           fabsf(yn1 == -INFINITY ? 0.f : yn1) > 0x1p20f)) {
+            const float mn0 = fmaxf(m0, yn0 - (Y0 + 10.f)), mn1 = fmaxf(m1, yn1 - (Y0 + 10.f));
+            y0 = fmaxf(y0, yn0 + 3.f);
+            y1 = fmaxf(y1, yn1 + 3.f);
+            hf0 = half_factor(m0, mn0);
+            hf1 = half_factor(m1, mn1);
+            m0 = mn0;
+            m1 = mn1;
+          } else {
+            // a becomes the largest score, rounded as the scores are, so that x - a is exact where the
+            // weight counts; b what x - a + e reaches, less 10
+            float4* pr = pairs + (warp * 4 + c4) * 2;
+            const float4 ab = were ? pr[0] : make_float4(m0, m1, 0.f, 0.f);
+            const float4 ff = were ? pr[1] : make_float4(f0, f1, 0.f, 0.f);
+            float a0 = ab.x, a1 = ab.y, b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                xs[t][b][0] = (__fmul_rn(xs[t][b][0], f0) - z0) / f0;
-                xs[t][b][1] = (__fmul_rn(xs[t][b][1], f1) - z1) / f1;
+                xs[t][b][0] = __fmul_rn(xs[t][b][0], ff.x);
+                xs[t][b][1] = __fmul_rn(xs[t][b][1], ff.y);
+                a0 = fmaxf(a0, xs[t][b][0]);
+                a1 = fmaxf(a1, xs[t][b][1]);
               }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+              a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float e = top_exponent(sv[t][b]) - Y0;
+                xs[t][b][0] -= a0;
+                xs[t][b][1] -= a1;
+                b0 = fmaxf(b0, xs[t][b][0] + e);
+                b1 = fmaxf(b1, xs[t][b][1] + e);
+              }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+              b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+            }
+            const float da0 = ab.x - a0, da1 = ab.y - a1;  // the old pair is a0 + (b + da0)
+            b0 = fmaxf(ab.z + da0, b0 - 10.f);
+            b1 = fmaxf(ab.w + da1, b1 - 10.f);
+            hf0 = ex2(0.5f * (da0 + (ab.z - b0)));
+            hf1 = ex2(0.5f * (da1 + (ab.w - b1)));
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                xs[t][b][0] -= b0;
+                xs[t][b][1] -= b1;
+              }
+            if (units >= 16) {  // the sums follow at once, so that their reference stays m
+              const float g0 = hf0 * hf0 * (r0 == m0 ? 1.f : ex2(r0 - m0)), g1 = hf1 * hf1 * (r1 == m1 ? 1.f : ex2(r1 - m1));
+#pragma unroll 1
+              for (int mt = 0; mt < 2 * NG; ++mt) {
+                const float4 v = sums[mt * 32 + lane];
+                sums[mt * 32 + lane] = make_float4(v.x * g0, v.y * g1, v.z * g0, v.w * g1);
+              }
+            }
+            r0 = r1 = m0 = m1 = 0.f;
             y0 = y1 = -INFINITY;
+            f0 = f1 = 1.f;
+            __syncwarp();
+            if (r == 0) {
+              pr[0] = make_float4(a0, a1, b0, b1);
+              pr[1] = ff;
+            }
+            __syncwarp();
           }
-          const float hf0 = half_factor(m0, mn0), hf1 = half_factor(m1, mn1);
           const float al0 = hf0 * hf0, al1 = hf1 * hf1;
-          m0 = mn0;
-          m1 = mn1;
           l0 = l0 * hf0 * hf0;
           l1 = l1 * hf1 * hf1;
 #pragma unroll
@@ -611,13 +669,11 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
             acc[mt][3] *= al1;
           }
         }
-        // (y at -inf: nothing seen, or m has been subtracted above)
-        const float mu0 = y0 == -INFINITY ? 0.f : m0, mu1 = y1 == -INFINITY ? 0.f : m1;
         // ---- O^T += (c - 8)^T . (p s)^T
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2(fmaf(xs[t][0][0], f0, -mu0)), p1 = ex2(fmaf(xs[t][0][1], f1, -mu1));
-          const float p2 = ex2(fmaf(xs[t][1][0], f0, -mu0)), p3 = ex2(fmaf(xs[t][1][1], f1, -mu1));
+          const float p0 = ex2(fmaf(xs[t][0][0], f0, -m0)), p1 = ex2(fmaf(xs[t][0][1], f1, -m1));
+          const float p2 = ex2(fmaf(xs[t][1][0], f0, -m0)), p3 = ex2(fmaf(xs[t][1][1], f1, -m1));
           l0 += p0 + p2;
           l1 += p1 + p3;
           uint32_t vw[4][NG / 2];
@@ -681,6 +737,22 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if (paired()) {
+      // relative to a alone: with a the largest score, l is at least 1 and the sums are those of 2^(x - a) V
+      const float4 ab = pairs[(warp * 4 + c4) * 2];
+      const float h0 = ex2(0.5f * ab.z), h1 = ex2(0.5f * ab.w);
+      l0 = l0 * h0 * h0;
+      l1 = l1 * h1 * h1;
+#pragma unroll
+      for (int mt = 0; mt < 2 * NG; ++mt) {
+        acc[mt][0] = acc[mt][0] * h0 * h0;
+        acc[mt][1] = acc[mt][1] * h1 * h1;
+        acc[mt][2] = acc[mt][2] * h0 * h0;
+        acc[mt][3] = acc[mt][3] * h1 * h1;
+      }
+      m0 = ab.x;
+      m1 = ab.y;
     }
     if constexpr (!WIDE) {
 #pragma unroll

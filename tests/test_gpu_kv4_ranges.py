@@ -87,3 +87,57 @@ def test_tokens_of_unlike_value_scales_all_count(order, split, large):
     v = bf16(rng.standard_normal((n, 1, d)) * np.where(is_large, large, 0.0)[:, None, None])
     got, K, V = run(q, k, v, bs, split)
     check(got, q, K, V)
+
+
+# ------------------------------------------------------------------ scores beyond any softmax
+@pytest.mark.parametrize("vs", [1e6, 1e-6, 1e-12, 1e25, 1e-25])
+@pytest.mark.parametrize("d,bs,G,split", [(128, 64, 4, 0), (64, 32, 8, 40), (64, 128, 1, 2)])
+def test_scores_beyond_any_softmax_with_values_far_from_one(vs, d, bs, G, split):
+    rng = np.random.default_rng(92)
+    n = 700
+    k, v = bf16(rng.standard_normal((n, 1, d)) * 1e4), bf16(rng.standard_normal((n, 1, d)) * vs)
+    q = bf16(rng.standard_normal((G, d)) * 1e5)
+    got, K, V = run(q, k, v, bs, split)
+    assert np.abs(R.values(q) @ K.T).max() * d**-0.5 > 1e8
+    check(got, q, K, V)
+
+
+@pytest.mark.parametrize("vs", [1e6, 1e-6, 1e-12])
+@pytest.mark.parametrize("what", [3e38, 1e8, "inf", "nan"])
+@pytest.mark.parametrize("G,split", [(4, 0), (8, 40)])
+def test_one_head_beyond_any_softmax_leaves_the_others_alone(vs, what, G, split):
+    """One head of a group with scores of 10^8 and more, or that is not finite; the others are ordinary."""
+    rng = np.random.default_rng(93)
+    n, d = 700, 64
+    k, v = bf16(rng.standard_normal((n, 1, d))), bf16(rng.standard_normal((n, 1, d)) * vs)
+    q = bf16(rng.standard_normal((G, d)))
+    if isinstance(what, str):
+        q[2, 5] = {"inf": 0x7F80, "nan": 0x7FC0}[what]
+    else:
+        q[2] = bf16(rng.uniform(-1, 1, d) * what)
+    got, K, V = run(q, k, v, 32, split)
+    check(got, q, K, V, [h for h in range(G) if h != 2])
+    if what == 1e8:
+        check(got, q, K, V, [2])
+    elif what == "nan":
+        assert np.isnan(got[2]).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("split", [4, 100])
+@pytest.mark.parametrize("vs", [1.0, 1e-9, 1e9])
+def test_scores_grow_beyond_any_softmax_on_the_way(sign, split, vs):
+    """A sequence whose later keys score 10^8 for the first head (or minus that), with values of unlike
+    scales: what was summed before, in registers and in shared memory, goes over to the new reference."""
+    rng = np.random.default_rng(94)
+    n, d, bs = 4900, 64, 64
+    k = rng.standard_normal((n, 1, d))
+    q = rng.standard_normal((4, d))
+    q[0] = np.abs(q[0])
+    late = rng.permutation(n - 3200)[:800] + 3200
+    k[late] = sign * np.abs(k[late]) * rng.uniform(0.5, 1, (800, 1, 1)) * 1e8
+    q[1:, :] -= (q[1:] @ np.ones(d))[:, None] / d
+    v = rng.standard_normal((n, 1, d)) * vs * 10.0 ** rng.uniform(-5, 5, (n, 1, 1))
+    q, k, v = bf16(q), bf16(k), bf16(v)
+    got, K, V = run(q, k, v, bs, split)
+    check(got, q, K, V)
