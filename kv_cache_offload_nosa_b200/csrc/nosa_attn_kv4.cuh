@@ -123,6 +123,10 @@ __device__ __forceinline__ uint32_t hfma2_u32(uint32_t x, uint32_t m, uint32_t a
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(m), "r"(a));
   return y;
 }
+__device__ __forceinline__ uint32_t mul_bf162(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
 // (x & m) | o in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
   uint32_t y;
@@ -440,6 +444,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
     // q as fp16 rows: each head's largest magnitude goes to [2^13, 2^14), so that what the
     // conversion drops is 2^-38 of it
     float f0, f1;
+    uint32_t down;  // 2^-e1, twice
     {
       const int qhead = col_head(r);
       const bool qok = qhead < a.G;
@@ -455,11 +460,22 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 2^e takes the largest there: any finite q down to 2^-87; below, e stays at 100, so that sums of
-      // up to 2^24 times a score are floats, and q loses digits
-      const int e = min(max(140 - static_cast<int>(mx >> 7), -114), 100);
+      // 2^e takes the largest there, or within fp16's range where that is more than 2^126 (q is below
+      // 2^-112, and still whole)
+      const int e = min(max(140 - static_cast<int>(mx >> 7), -114), 126);
       const float up = __uint_as_float((127 + e) << 23);
-      const float fq = __uint_as_float((127 - e) << 23) * a.scale_log2;
+      // The sums with q 2^e are up to 2^22 times K's scale: beyond fp32 for large keys of small queries,
+      // although the scores are ordinary. So K's scales are taken times 2^-e1 (exact in bf16; it costs
+      // nothing that could be measured on long axes), e1 being the least e of the group's finite heads
+      // and at least 0: the sums are then no larger than that head's scores, the group's largest, and
+      // what a scale loses below 2^-126 changes no score by 2^-100.
+      const uint32_t top = __reduce_max_sync(0xffffffffu, mx < 0x7f80u ? mx : 0u);
+      const int e1 = min(max(140 - static_cast<int>(top >> 7), 0), 126);
+      down = static_cast<uint32_t>(127 - e1) << 7;
+      down |= down << 16;
+      // (above zero, so that a masked score's -inf stays one)
+      const float fq = fmaxf(
+          __uint_as_float((127 + e1) << 23) * __uint_as_float((127 - e) << 23) * a.scale_log2, 0x1p-126f);
       // from column r of B (all four c4 lanes agree) to columns 2 c4, 2 c4 + 1 of C
       f0 = __shfl_sync(0xffffffffu, fq, 8 * c4);
       f1 = __shfl_sync(0xffffffffu, fq, 8 * c4 + 4);
@@ -525,6 +541,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             lds_words<NG / 2>(st + offS + (16 * t + 8 * b) * (D / 16), sk[b]);
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g) sk[b][g] = mul_bf162(sk[b][g], down);
             lds_words<NG / 2>(st + SH::PAGE + offS + (16 * t + 8 * b) * (D / 16), sv[t][b]);
             xs[t][b][0] = xs[t][b][1] = 0.f;
           }

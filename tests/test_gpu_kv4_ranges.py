@@ -141,3 +141,34 @@ def test_scores_grow_beyond_any_softmax_on_the_way(sign, split, vs):
     q, k, v = bf16(q), bf16(k), bf16(v)
     got, K, V = run(q, k, v, bs, split)
     check(got, q, K, V)
+
+
+# ------------------------------------------------------------------ keys at the ends of the range
+@pytest.mark.parametrize("qs,ks", [(1e-36, 1e36), (1e-33, 1e37), (1e-30, 3e32), (1e-37, 1.0), (3e-39, 1e38), (1e33, 1e-33),
+                                   (1e37, 1e-37)])
+def test_keys_and_queries_at_the_ends_of_the_range(qs, ks):
+    """Ordinary scores of very large and very small keys and queries."""
+    rng = np.random.default_rng(95)
+    n, d = 500, 128
+    k, v = bf16(rng.uniform(-3, 3, (n, 1, d)) * ks), bf16(rng.standard_normal((n, 1, d)))
+    q = bf16(rng.standard_normal((4, d)) * qs)
+    got, K, V = run(q, k, v, 64)
+    check(got, q, K, V)
+
+
+@pytest.mark.parametrize("other", [1e-38, 1e-30, 1.0, "zero", "nan", "inf"])
+def test_large_keys_with_unlike_heads(other):
+    """Keys of 10^36 with ordinary scores for one head, beside a head that is far smaller, far larger
+    (scores of 10^37, finite in fp32), zero or not finite."""
+    rng = np.random.default_rng(96)
+    n, d = 500, 64
+    k, v = bf16(rng.standard_normal((n, 1, d)) * 1e36), bf16(rng.standard_normal((n, 1, d)))
+    q = bf16(rng.standard_normal((2, d)) * 1e-36)
+    if isinstance(other, str):
+        q[1] = {"zero": 0, "inf": 0x7F80, "nan": 0x7FC0}[other]
+    else:
+        q[1] = bf16(rng.standard_normal(d) * other)
+    got, K, V = run(q, k, v, 32)
+    check(got, q, K, V, [0] if other in ("nan", "inf") else [0, 1])
+    if other == "nan":
+        assert np.isnan(got[1]).all()
