@@ -357,7 +357,7 @@ nosa_status nosa_attend(const nosa_config* cfg, const nosa_state* st, const uint
  * split-K partials and the per-group counters) lives in a static device array of 8 MiB
  * inside the library, which every GPU that loads the library keeps until the process exits.
  * Limit: B*Hkv * (16 * G * (d + 2) * 4 bytes, rounded up to 256; with kv_bits = 4 the 2 * G
- * floats beside the G * d are rounded up to 4) plus B*Hkv * 4 bytes must
+ * floats beside the G * d are rounded up to 4, and up to 73 groups always fit) plus B*Hkv * 4 bytes must
  * fit in 8 MiB (about 250 groups at G = 4, d = 128); larger configurations get NOSA_ENOMEM and
  * must use nosa_decode_attn with a workspace. Allocates nothing: no cudaMalloc, no cudaFree.
  * The first call on each device looks up the array's device address (cudaGetSymbolAddress)

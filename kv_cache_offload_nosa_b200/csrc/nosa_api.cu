@@ -1173,7 +1173,9 @@ extern "C" nosa_status nosa_decode_attn_noalloc(const nosa_config* cfg, const no
              "q/sel/out NULL or misaligned");
   NOSA_CHECK(!(c.stop_tau > 0.f), "early stop visits blocks by the step's scores: use nosa_step");
   const size_t NG = n_groups(c);
-  const size_t part_bytes = up256(partial_bytes(c, kPartialSlots));
+  // the same slots, and so the same split, as with a workspace (at 4-bit pages more than 16 a group only
+  // where that is 1256 in all: 5.2 MB at most)
+  const size_t part_bytes = up256(partial_bytes(c, part_slots(c)));
   const size_t need = part_bytes + up256(NG * 4);
   if (need > kNoAllocScratchBytes)
     return fail(NOSA_ENOMEM, "nosa_decode_attn_noalloc needs %zu bytes of static scratch; the limit is %zu "
@@ -1188,7 +1190,7 @@ extern "C" nosa_status nosa_decode_attn_noalloc(const nosa_config* cfg, const no
   // the array keeps the previous call's contents: the last-arriver counters must start at zero
   NOSA_CUDA(cudaMemsetAsync(counters, 0, NG * 4, s));
   const AttnArgs a = attn_args(c, st, q, sel, out, static_cast<float*>(base), counters);
-  if (kv4(c)) return launch_attn_kv4(c, st, a, kPartialSlots, s, /*finest=*/false, /*pdl=*/true);
+  if (kv4(c)) return launch_attn_kv4(c, st, a, part_slots(c), s, /*finest=*/false, /*pdl=*/true);
   return dispatch_attn(c, a, tk, tv, s, /*finest=*/false, /*pdl=*/true);
 }
 

@@ -172,3 +172,24 @@ def test_large_keys_with_unlike_heads(other):
     check(got, q, K, V, [0] if other in ("nan", "inf") else [0, 1])
     if other == "nan":
         assert np.isnan(got[1]).all()
+
+
+# ------------------------------------------------------------------ without a workspace
+@pytest.mark.parametrize("B,G,Hkv,d,bs,k", [(1, 4, 1, 128, 64, 300), (1, 8, 2, 64, 32, 500), (5, 4, 8, 128, 32, 70),
+                                            (73, 1, 1, 64, 64, 40)])
+def test_noalloc_attention_is_the_same_bit_for_bit(B, G, Hkv, d, bs, k):
+    rng = np.random.default_rng(97)
+    n = k * bs - 5
+    cache = nosa.NosaCache(nosa.make_config(B, G * Hkv, Hkv, d, bs, 32, k, 0, k, kv_bits=4))
+    gen = torch.Generator(device="cuda").manual_seed(97)
+    k_, v_ = (torch.randn(B * n, Hkv, d, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    cache.write(k_, v_, torch.arange(B + 1, dtype=torch.int32, device="cuda") * n)
+    cache.init(torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    q = dev(bf16(rng.standard_normal((B, G * Hkv, d))))
+    sel = torch.arange(k, dtype=torch.int32, device="cuda").repeat(B * Hkv, 1)
+    out, same = (torch.full((B, G * Hkv, d), float("nan"), device="cuda") for _ in range(2))
+    for _ in range(2):
+        cache.decode_attn(q, sel, out)
+        nosa.decode_attn_noalloc(cache.cfg, cache.state, q, sel, same)
+        assert torch.equal(out, same)
+    assert cache.check() == (nosa.NOSA_OK, 0)
