@@ -58,7 +58,11 @@ def check_run(cfg: nosa_config, k: torch.Tensor, v: torch.Tensor, cu_tokens, sta
     """Refuses (NosaError, NOSA_EINVAL) what is not a run of tokens on `device`: k and v
     [n_tokens, Hkv, d] of 16-bit values with contiguous rows, cu_tokens [B + 1] and start [B]
     (or None) int32 and contiguous. Returns the rows' strides, None where both are contiguous."""
-    index, B, i32 = device.index, cfg.B, torch.int32
+    index, B, i32, T = device.index, cfg.B, torch.int32, torch.Tensor
+    if not (isinstance(k, T) and isinstance(v, T) and isinstance(cu_tokens, T) and (start is None or isinstance(start, T))):
+        for name, t in (("k", k), ("v", v), ("cu_tokens", cu_tokens), ("start", start)):
+            if not isinstance(t, T):
+                raise NosaError(NOSA_EINVAL, f"{name} must be a CUDA tensor, not {type(t).__name__}")
     want = (k.shape[0] if k.dim() else 0, cfg.Hkv, cfg.d)
     if not (k.shape == want and v.shape == want and k.dtype in _ROW_TYPES and v.dtype in _ROW_TYPES and
             k.get_device() == index and v.get_device() == index):

@@ -196,3 +196,20 @@ def test_split_of_a_4_bit_cache(lib):
     assert g(B=8, Hq=16, Hkv=16, d=64, block_size=32, k_q=77, k_e=0, max_blocks=256) == (26, 384)
     assert g(B=6, Hq=64, Hkv=8, block_size=128, k_q=24, k_e=0, max_blocks=128) == (4, 288)
     assert g(B=1, Hq=8, Hkv=2, d=64, k_q=16, k_e=0, max_blocks=65) == (1, 32)
+
+
+@pytest.mark.parametrize("name", ["k", "v", "cu_tokens", "start"])
+@pytest.mark.parametrize("what", [None, 0x100000, [0, 1, 2]])
+def test_what_is_not_a_tensor_is_refused(name, what):
+    i32 = torch.int32
+    run = dict(k=on_cuda(5, 2, 128), v=on_cuda(5, 2, 128), cu_tokens=on_cuda(3, dtype=i32), start=on_cuda(2, dtype=i32))
+    run[name] = what
+    cache = NosaCache.__new__(NosaCache)
+    cache.cfg, cache.device = cfg(), torch.device("cuda", 0)
+    if name == "start" and what is None:
+        assert check_run(cache.cfg, *run.values(), cache.device) is None
+        return
+    for call in (cache.write, cache.read):
+        with pytest.raises(nosa.NosaError) as e:
+            call(**run)
+        assert e.value.status == nosa.NOSA_EINVAL and name in str(e.value)
