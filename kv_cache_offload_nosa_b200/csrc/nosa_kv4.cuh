@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t kv4_scale(uint32_t amax) {
 }
 // The multiplier that takes a value to its code minus 8.
 __device__ __forceinline__ float kv4_inverse(uint32_t scale) {
-  float r;  // within 2^-23 (s is normal, at least 2^-126, and its reciprocal at least 2^-125)
+  float r;  // within 2^-23 (s is normal, 2^-126 to 2^125.2, and so is its reciprocal)
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float(scale << 16)));
   return scale == 0u ? 0.f : r * (1.0f + 0x1p-20f);
 }

@@ -207,6 +207,39 @@ def test_rows_of_no_sequence_and_positions_outside_are_skipped():
     assert (ko[[t for t in range(40) if t not in skip]] != 7).any()
 
 
+@pytest.mark.parametrize("d,bs,offload", [(64, 32, False), (128, 64, True)])
+def test_what_is_skipped_touches_neither_pool_and_the_rest_comes_back(d, bs, offload):
+    """Tokens of no sequence and positions outside the cache, in K and in V: pages and rows read."""
+    rng = np.random.default_rng(13)
+    k, v = bf16_rows(rng, 40, 2, d), bf16_rows(rng, 40, 2, d)
+    cache = make_cache(3, 4, 2, d, bs, 4, 1, offload=offload, slots=3 if offload else None)
+    for p in pools(cache):
+        p.fill_(0xA5)
+    end = 4 * bs
+    cu, start = np.array([4, 10, 20, 30], np.int32), np.array([0, end - 4, -4], np.int32)
+    cache.write(dev(k), dev(v), dev(cu), dev(start))
+    assert cache.check() == (nosa.NOSA_EDEVICE, nosa.ERR_FULL)
+    want = []
+    for bits, keys in ((k, True), (v, False)):
+        C, S = R.unpack(np.full((6, 4, bs * d * 9 // 16), 0xA5, np.uint8), bs, d, keys)
+        C, S = C.reshape(6, end, d // 32, 32), S.reshape(6, end, d // 32)
+        codes, scales = R.quantise(bits)
+        for h in range(2):
+            C[h, 0:6], S[h, 0:6] = codes[4:10, h], scales[4:10, h]
+            C[2 + h, end - 4:], S[2 + h, end - 4:] = codes[10:14, h], scales[10:14, h]
+            C[4 + h, 0:6], S[4 + h, 0:6] = codes[24:30, h], scales[24:30, h]
+        want.append((C, S, np.zeros(C.shape[:3], bool)))
+    check_pages(cache, want)
+    ko, vo = (torch.full((40, 2, d), 7, dtype=torch.int16, device="cuda") for _ in range(2))
+    cache.read(ko, vo, dev(cu), dev(start))
+    held_ = [*range(4, 14), *range(24, 30)]
+    for got, bits in ((ko, k), (vo, v)):
+        got = got.cpu().numpy().view(np.uint16)
+        ref = np.full_like(got, 7)
+        ref[held_] = R.round_to_bf16(R.dequantise(*R.quantise(bits)))[held_]
+        assert np.array_equal(np.where(got == 0x8000, 0, got), np.where(ref == 0x8000, 0, ref))
+
+
 def test_write_to_host_pools():
     rng = np.random.default_rng(11)
     k, v = hard_rows(rng, 400, 2, 128), hard_rows(rng, 400, 2, 128)
