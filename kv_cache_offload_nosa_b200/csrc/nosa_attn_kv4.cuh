@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       const int e1 = min(max(140 - static_cast<int>(top >> 7), 0), 126);
       down = static_cast<uint32_t>(127 - e1) << 7;
       down |= down << 16;
+      if (WIDE && lane == 0) s_flag[1] = static_cast<int>(down);  // the same from every warp
       // (above zero, so that a masked score's -inf stays one)
       const float fq = fmaxf(
           __uint_as_float((127 + e1) << 23) * __uint_as_float((127 - e) << 23) * a.scale_log2, 0x1p-126f);
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
         // ---- scores of two tiles of 16 tokens: [tile][row A, row B][column]
         float xs[2][2][2];
         uint32_t sv[2][2][NG / 2];
+        const uint32_t dn = WIDE ? static_cast<uint32_t>(s_flag[1]) : down;  // (no register left for it)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           uint32_t ka[NG], kb[NG], sk[2][NG / 2];
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
           for (int b = 0; b < 2; ++b) {
             lds_words<NG / 2>(st + offS + (16 * t + 8 * b) * (D / 16), sk[b]);
 #pragma unroll
-            for (int g = 0; g < NG / 2; ++g) sk[b][g] = mul_bf162(sk[b][g], down);
+            for (int g = 0; g < NG / 2; ++g) sk[b][g] = mul_bf162(sk[b][g], dn);
             lds_words<NG / 2>(st + SH::PAGE + offS + (16 * t + 8 * b) * (D / 16), sv[t][b]);
             xs[t][b][0] = xs[t][b][1] = 0.f;
           }
