@@ -419,15 +419,15 @@ int attn_split_for(int split, int k, int total, long long target, int sms, int s
   return W;
 }
 
-// The same for 4-bit pages. Unpacking bounds the kernel, and the CTAs of an SM share its issue slots,
-// so an even load counts: every CTA that the GPU holds at once gets the same number of tasks, wherever
+// The same for 4-bit pages. Unpacking them costs more than fetching them, and the CTAs of an SM share its
+// units, so an even load counts: every CTA that the GPU holds at once gets the same number of tasks, wherever
 // that cuts a group (2048 blocks of 64 tokens, 32 groups, d = 128, 444 CTAs: 147 us in even shares of
-// 148, 153 us in ranges of 158 within the groups, 180 us in ranges of 128). But a CTA with parts of two
+// 148, 162 us in ranges of 158 within the groups, 179 us in ranges of 128). But a CTA with parts of two
 // groups starts and ends a part twice, about 3 us. Ranges within the groups (parts > 0) are taken where
 // they leave no SM more than 96 Ki values of K rows over the even share, which is what it unpacks in
-// that time (64 blocks, 128 groups: 29.4 against 30.4 us; 2048 blocks, 8 groups: 48.0 against 49.7 us;
-// 77 blocks of 32 tokens, 128 groups, d = 64: 14.4 against 16.7 us). With fewer than about two CTAs an
-// SM nothing covers their latencies (the last case with one range a group: 17.7 us).
+// that time (64 blocks, 128 groups: 28.9 against 30.6 us; 2048 blocks, 8 groups: 47.9 against 48.8 us;
+// 77 blocks of 32 tokens, 128 groups, d = 64: 14.1 against 16.3 us). With fewer than about two CTAs an
+// SM nothing covers their latencies (the last case with one range a group: 17.1 us).
 // finest: ranges within the groups too, up to 16 each.
 struct Kv4Split {
   int W, parts, ctas;

@@ -8,11 +8,14 @@
 // ring of stages; the consumer warps take 32 tokens each, a page's units going to neighbouring warps and
 // page after page to the next.
 //
-// Bound: the pages are 3.6 times smaller than bf16 ones, so unpacking them bounds the kernel before
-// memory does. Per 16 tokens (d = 128) a warp issues about 370 instructions, 146 of them on the integer
-// pipe (two cycles each). Over four sequences of 131072 tokens, 8 KV heads of 4 query heads each, it
-// takes 147 us (4.1 TB/s; the same pages copied and not unpacked: 97 us); what counts is instructions,
-// not warps (8 or 12 consumer warps an SM take the same time). mma.sync and not tcgen05: a group has
+// Time: the pages are 3.6 times smaller than bf16 ones, so it is unpacking them that costs, not memory.
+// Over four sequences of 131072 tokens, 8 KV heads of 4 query heads each, it takes 147 us replayed from a
+// graph and up to 156 us in other company (4.1 to 3.9 TB/s; the same pages copied and not unpacked: 97
+// us), over one of them 48 us. There a warp issues 390 instructions per 16 tokens, start, end and merge
+// included, and no unit is full: issue slots 55 %, integer pipe 43 %, shared memory 33 % (58 wavefronts
+// per 16 tokens and warp, 17 of them bank conflicts), FMA pipe 33 %, tensor pipe 18 %. Fewer
+// instructions made it faster, more warps did not (8 or 12 consumer warps an SM take the same time);
+// what leaves the other issue slots empty has not been found. mma.sync and not tcgen05: a group has
 // G <= 8 query rows, and codes have to pass through registers on their way to an operand.
 //
 // The pages are never expanded. With s the scales and c the codes,
@@ -29,7 +32,9 @@
 // about the base-2 logarithm of the token's largest V scale, and it moves only when an x_t + e_t
 // exceeds it by more than 13. Weights are thus below 2^15, and one of 2^-14 of the largest still
 // has all 22 bits of its two parts. (e_t is at least -90, which keeps p and its sum finite: V below
-// 2^-100 loses digits, and below 2^-120 vanishes. Above 2^112 weights under 2^-11 of the largest do.)
+// 2^-100 loses digits, and below 2^-120 vanishes. With scales of 2^e weights under 2^(e - 136) of the
+// largest do, 2^-11 at most. In a group 2^n smaller than the row's largest, n > 13, the parts' last place,
+// 2^-35 of the largest weight, is about 2^(n-35) of the result.)
 // Beyond 2^20 a score plus e_t is not e_t precise enough, and a warp that meets one there carries its
 // references as pairs a + b: a near the scores and taken from them first, b for the scales of V.
 #pragma once
@@ -124,7 +129,8 @@ __device__ __forceinline__ uint32_t hfma2_u32(uint32_t x, uint32_t m, uint32_t a
   return y;
 }
 __device__ __forceinline__ uint32_t mul_bf162(uint32_t x, uint32_t y) {
-  const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  const __nv_bfloat162 z =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 // (x & m) | o in one instruction.
@@ -759,7 +765,8 @@ __global__ void __launch_bounds__(AttnKv4Shape<D, BS>::THREADS, AttnKv4Shape<D, 
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
     if (paired()) {
-      // relative to a alone: with a the largest score, l is at least 1 and the sums are those of 2^(x - a) V
+      // relative to a alone: with a the largest score, l is at least 1 and the sums are those of
+      // 2^(x - a) V, floats for V up to 2^107 (of less than 2^20 tokens)
       const float4 ab = pairs[(warp * 4 + c4) * 2];
       const float h0 = ex2(0.5f * ab.z), h1 = ex2(0.5f * ab.w);
       l0 = l0 * h0 * h0;

@@ -174,6 +174,24 @@ def test_large_keys_with_unlike_heads(other):
         assert np.isnan(got[1]).all()
 
 
+@pytest.mark.parametrize("n", [6, 13, 20])
+def test_groups_of_unlike_scales_within_a_row(n):
+    """A group of 32 values 2^n times smaller than the others of its rows. The largest weight p s is at
+    least 2^10 for the largest scale, and each of N weights is off by the ordinary bound and by half the
+    last place of fp16, 2^-25: N 2^-35 of the row's largest value."""
+    rng = np.random.default_rng(98)
+    N, d = 300, 128
+    k, q = bf16(rng.standard_normal((N, 1, d))), bf16(rng.standard_normal((4, d)))
+    v = rng.standard_normal((N, 1, d))
+    v[..., 32:64] *= 2.0**-n
+    got, K, V = run(q, k, bf16(v), 64)
+    scale = float(np.float32(d**-0.5))
+    want = R.attend(R.values(q), K, V, scale)
+    tol = R.attend_bound(R.values(q), K, V[:, 32:64], scale) + N * 2.0**-35 * np.abs(V).max()
+    assert (np.abs(got - want)[:, 32:64].max(-1) <= tol).all()
+    check(got, q, K, V)
+
+
 # ------------------------------------------------------------------ without a workspace
 @pytest.mark.parametrize("B,G,Hkv,d,bs,k", [(1, 4, 1, 128, 64, 300), (1, 8, 2, 64, 32, 500), (5, 4, 8, 128, 32, 70),
                                             (73, 1, 1, 64, 64, 40)])
