@@ -50,7 +50,8 @@
  * nosa_read_kv brings tokens back, and the attention reads the pages as they are. Sub-block
  * means (kc) are over the values that the cache holds.
  * Range of the attention over these pages: queries of any finite size; sums of |q_i k_i| over a row
- * below 2^127; rows of V whose largest value is 0 or within 2^-100 to 2^107. (Smaller ones lose
+ * below 2^127; rows of V whose largest value is 0 or within 2^-100 to 2^107. (Tokens whose weight is
+ * below 2^-126 of the largest may count as none, as in any softmax in fp32. Smaller values of V lose
  * digits, and below 2^-120 count as zeros; beside larger ones weights under 2^-11 of the largest may
  * count as none, and above 2^107 scores beyond 2^20 may give infinities.) Weights are held to 22
  * bits beside the largest value of their row of V: a group of 32 values 2^n times smaller than that,

@@ -179,8 +179,9 @@ __device__ __forceinline__ float half_factor(float from, float to) { return from
 
 // The last CTA of a group merges its partials p0 [nseg] into outg [G][D]: the segments' shares of the
 // weights (a head per warp, a segment per lane) with the first values under way, then every NC-th
-// segment per warp, the warps' sums last. scr: shared memory for [G] x 128 shares and [NC][G][D] values.
-// Two meetings. Out of line: its registers would cost the main loop.
+// segment per warp, the warps' sums last. (A share below 2^-126 is zero, as in any fp32 softmax.) scr:
+// shared memory for [G] x 128 shares and [NC][G][D] values. Two meetings. Out of line: its registers
+// would cost the main loop.
 template <int D, int NC, bool WIDE>
 __device__ __noinline__ bool kv4_merge(const float* p0, float* outg, float* scr, int nseg, int G, uint64_t* meet,
                                        uint32_t met, unsigned long long deadline) {
